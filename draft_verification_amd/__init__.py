@@ -22,6 +22,12 @@ from ._lib import (  # noqa: F401
     sd_uniforms,
     sd_lightspec_update,
     sd_lightspec_plan,
+    sd_logit_shape,
+    sd_token_counts,
+    sd_slot_reserve,
+    sd_slot_reserve_workspace_size,
+    sd_slot_commit,
+    sd_slot_commit_workspace_size,
     SD_SCHED_EARLY_STOP,
     SD_SCHED_GLOBAL_ARGMAX,
     SD_SCHED_CAPPED_TOPK,
@@ -32,4 +38,6 @@ from ._lib import (  # noqa: F401
     SD_ST_ZERO_Z,
     SD_ST_ZERO_RESIDUAL,
     SD_ST_ZERO_Q,
+    SD_ST_BAD_INPUT,
+    SD_ST_NO_SLOT,
 )

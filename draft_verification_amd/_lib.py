@@ -37,6 +37,8 @@ SD_ST_NONFINITE = 2
 SD_ST_ZERO_Z = 4
 SD_ST_ZERO_RESIDUAL = 8
 SD_ST_ZERO_Q = 16
+SD_ST_BAD_INPUT = 32
+SD_ST_NO_SLOT = 64
 
 EXPORTS = (
     "sd_abi_version", "sd_status_string", "sd_schedule_workspace_size", "sd_schedule",
@@ -45,6 +47,8 @@ EXPORTS = (
     "sd_rnn_draft_workspace_size", "sd_rnn_draft",
     "sd_lightspec_update", "sd_lightspec_plan_workspace_size", "sd_lightspec_plan",
     "sd_uniforms", "sd_verify_noalloc",
+    "sd_logit_shape", "sd_token_counts", "sd_slot_reserve_workspace_size", "sd_slot_reserve",
+    "sd_slot_commit_workspace_size", "sd_slot_commit",
 )
 
 
@@ -104,6 +108,22 @@ def lib():
                                     _P, _P, _P, _P, _P, _P, _P, _P, _P, _I]
     L.sd_uniforms.restype = _I
     L.sd_uniforms.argtypes = [_P, _U64, ctypes.c_longlong, _P, _P, _I, _P]
+    L.sd_logit_shape.restype = _I
+    L.sd_logit_shape.argtypes = [_P, _I, _I, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P, _I,
+                                 _I, _P, _P, _P, _P, ctypes.c_longlong, _P, _I, _I, _P, _P]
+    L.sd_token_counts.restype = _I
+    L.sd_token_counts.argtypes = [_P, _I, _I, _P, ctypes.c_longlong, _I, _P, _P, _P, _P, _P, _P, _I, _P, _I,
+                                  _I, _P]
+    L.sd_slot_reserve_workspace_size.restype = _SZ
+    L.sd_slot_reserve_workspace_size.argtypes = [_I]
+    L.sd_slot_reserve.restype = _I
+    L.sd_slot_reserve.argtypes = [_P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P,
+                                  _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ]
+    L.sd_slot_commit_workspace_size.restype = _SZ
+    L.sd_slot_commit_workspace_size.argtypes = [_I]
+    L.sd_slot_commit.restype = _I
+    L.sd_slot_commit.argtypes = [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                 _P, _P, _P, _SZ]
     _lib = L
     return L
 
@@ -412,3 +432,258 @@ def sd_lightspec_plan(ema, count, d_prev, sps, draft_cost, out=None, workspace=N
         _ptr(phi, torch.float64), ws.data_ptr(), ws.numel()))
     return dict(conf=conf, ell=ell, batch=batch, n_sel=n_sel, theta=theta, d_next=d_next,
                 b_next=b_next, phi=phi)
+
+
+def _on_device(fn):
+    """Run fn with the device of its first argument as torch's current one, so
+    that the kernels are launched, and outputs made, where the tensors live;
+    a given stream has to be that device's."""
+    name = next(iter(inspect.signature(fn).parameters))
+
+    @functools.wraps(fn)
+    def wrapper(*args, **kw):
+        dev = getattr(args[0] if args else kw.get(name), "device", None)
+        if dev is None or dev.type != "cuda":
+            return fn(*args, **kw)   # which refuses it
+        stream = kw.get("stream")
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        if dev.index == torch.cuda.current_device():
+            return fn(*args, **kw)
+        with torch.cuda.device(dev):
+            return fn(*args, **kw)
+    return wrapper
+
+
+def _ptr_on(t, dtype, name, dev, shape=None):
+    """The address of tensor t (None: NULL) after checking its type, its
+    device, that it is contiguous, and its shape where given."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must live on {dev}, not {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _device_of(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must live on the GPU")
+    return t.device
+
+
+def _state_rows(seen, counts, V):
+    """(n_slots, ld_seen, ld_counts) of a token state; 0 where there is none."""
+    if seen is None:
+        if counts is not None:
+            raise ValueError("counts need seen")
+        return 0, 0, 0
+    if seen.dim() != 2 or (counts is not None and (counts.dim() != 2 or counts.shape[0] != seen.shape[0])):
+        raise ValueError("seen and counts must be 2-D with one row per slot")
+    return seen.shape[0], seen.shape[1], 0 if counts is None else counts.shape[1]
+
+
+@_on_device
+@_on_stream
+def sd_logit_shape(logits, row0, ell, V, gamma_max=None, draft_tokens=None, repetition=None, frequency=None,
+                   presence=None, seen=None, counts=None, slot=None, bias=None, mask=None, mask_row0=None,
+                   out=None, *, stream=None):
+    """Apply penalties, biases and grammar masks to the rows of a verify batch.
+    logits: 2-D rows (bf16 or fp32, ld = shape[1]); row0, ell [R] int32 as for
+    sd_verify (ell < 0: no rows); draft_tokens [R][gamma_max] int32, or None
+    with gamma_max given.  repetition, frequency, presence [R] fp32; seen
+    [n_slots][words] int32 and counts [n_slots][ld] int32 as sd_token_counts
+    keeps them; slot [R] int32.  bias: (offsets [R + 1] int64, tokens int32,
+    values fp32).  mask [rows][words] int32 with mask_row0 [R] int32.
+    out["logits"] may be logits itself (in place); without it new rows are
+    made, whose parts outside the batch are undefined.  Returns a dict of
+    device tensors: logits, status."""
+    dev = _device_of(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D")
+    n_rows, ld = logits.shape
+    R = row0.numel()
+    if draft_tokens is not None:
+        if draft_tokens.dim() != 2 or gamma_max not in (None, draft_tokens.shape[1]):
+            raise ValueError("draft_tokens must be [R][gamma_max]")
+        gamma_max = draft_tokens.shape[1]
+    elif gamma_max is None:
+        raise ValueError("gamma_max is needed without draft_tokens")
+    if logits.dtype is torch.bfloat16:
+        dt = SD_DTYPE_BF16
+    elif logits.dtype is torch.float32:
+        dt = SD_DTYPE_F32
+    else:
+        raise TypeError("logits must be bf16 or fp32")
+    n_slots, ld_seen, ld_counts = _state_rows(seen, counts, V)
+    b_off, b_tok, b_val = (None, None, None) if bias is None else bias
+    if (mask is None) != (mask_row0 is None):
+        raise ValueError("mask and mask_row0 go together")
+    if mask is not None and mask.dim() != 2:
+        raise ValueError("mask must be 2-D")
+    o = out or {}
+    dst = _out(o, "logits", lambda: torch.empty_like(logits))
+    status = _out(o, "status", lambda: torch.empty(R, dtype=torch.int32, device=dev))
+    i32, f32, n = torch.int32, torch.float32, (R,)
+    code = lib().sd_logit_shape(
+        _stream(stream), R, int(gamma_max), int(V), ld, dt, _ptr_on(logits, logits.dtype, "logits", dev),
+        _ptr_on(dst, logits.dtype, "out", dev, logits.shape), n_rows, _ptr_on(row0, i32, "row0", dev),
+        _ptr_on(ell, i32, "ell", dev, n),
+        None if draft_tokens is None else _ptr_on(draft_tokens, i32, "draft_tokens", dev, (R, gamma_max)),
+        _ptr_on(repetition, f32, "repetition", dev, n), _ptr_on(frequency, f32, "frequency", dev, n),
+        _ptr_on(presence, f32, "presence", dev, n), _ptr_on(seen, i32, "seen", dev), ld_seen,
+        _ptr_on(counts, i32, "counts", dev), ld_counts, n_slots, _ptr_on(slot, i32, "slot", dev, n),
+        _ptr_on(b_off, torch.int64, "bias offsets", dev, (R + 1,)), _ptr_on(b_tok, i32, "bias tokens", dev),
+        None if bias is None else _ptr_on(b_val, f32, "bias values", dev, b_tok.shape),
+        0 if bias is None else b_tok.numel(), _ptr_on(mask, i32, "mask", dev),
+        0 if mask is None else mask.shape[1], 0 if mask is None else mask.shape[0],
+        _ptr_on(mask_row0, i32, "mask_row0", dev, n), _ptr_on(status, i32, "status", dev, n))
+    _check("sd_logit_shape", code)
+    return dict(logits=dst, status=status)
+
+
+@_on_device
+@_on_stream
+def sd_token_counts(tokens, seen, counts, V, start=None, length=None, prompt_len=None, slot=None, reset=None,
+                    out=None, *, stream=None):
+    """Enter token lists into the state behind the penalties, in place: seen
+    [n_slots][words] int32 (bits), counts [n_slots][ld] int32 or None.
+    tokens: [R][width] int32 (entries outside [0, V) are skipped, such as the
+    -1 behind sd_verify's tokens), with length [R] int32 or None; or 1-D with
+    start [R] int64 and length.  prompt_len [R] int32: how many leading tokens
+    of each list are prompt; reset [R] int32: clear the state row first.
+    Returns a dict: status."""
+    dev = _device_of(tokens, "tokens")
+    if start is not None:
+        R, width = start.numel(), 0
+        if length is None:
+            raise ValueError("start needs length")
+    else:
+        if tokens.dim() != 2:
+            raise ValueError("tokens must be [R][width] without start")
+        R, width = tokens.shape
+    if seen is None:
+        raise ValueError("seen is needed")
+    n_slots, ld_seen, ld_counts = _state_rows(seen, counts, V)
+    status = _out(out or {}, "status", lambda: torch.empty(R, dtype=torch.int32, device=dev))
+    i32, n = torch.int32, (R,)
+    code = lib().sd_token_counts(
+        _stream(stream), R, int(V), _ptr_on(tokens, i32, "tokens", dev), tokens.numel(), width,
+        _ptr_on(start, torch.int64, "start", dev), _ptr_on(length, i32, "length", dev, n),
+        _ptr_on(prompt_len, i32, "prompt_len", dev, n), _ptr_on(slot, i32, "slot", dev, n),
+        _ptr_on(reset, i32, "reset", dev, n), _ptr_on(seen, i32, "seen", dev), ld_seen,
+        _ptr_on(counts, i32, "counts", dev), ld_counts, n_slots, _ptr_on(status, i32, "status", dev, n))
+    _check("sd_token_counts", code)
+    return dict(status=status)
+
+
+def sd_slot_reserve_workspace_size(R):
+    return lib().sd_slot_reserve_workspace_size(R)
+
+
+@_on_device
+@_on_stream
+def sd_slot_reserve(seq_len, ell, block_table, free_list, free_count, block_size, q_max, max_rows=None,
+                    padded=False, x0=None, tokens=None, out=None, workspace=None, *, stream=None):
+    """Rows and cache slots of a step.  seq_len [R] int64, ell [R] int32
+    (rows - 1 asked for; -1: none), block_table [R][max_blocks] int32 (new
+    blocks are entered in place), free_list [n_blocks] int32, free_count [1]
+    int32.  x0 [R] and / or tokens [R][n] int32 give the rows' tokens.
+    max_rows: rows of the buffers (default R * q_max, or those of
+    out["row_req"]).  Returns a dict of device tensors: ell, row0, cu_rows,
+    ctx_len, batch, free_count, row_req, row_pos, row_slot, row_token (None
+    without tokens), status."""
+    dev = _device_of(seq_len, "seq_len")
+    R = seq_len.numel()
+    if block_table.dim() != 2 or (tokens is not None and tokens.dim() != 2):
+        raise ValueError("block_table and tokens must be 2-D")
+    mb = block_table.shape[1]
+    o = out or {}
+    i32 = torch.int32
+    if max_rows is None:
+        max_rows = o["row_req"].numel() if "row_req" in o else R * q_max
+    make = lambda k, dt=i32: (lambda: torch.empty(k, dtype=dt, device=dev))  # noqa: E731
+    res = dict(ell=_out(o, "ell", make(R)), row0=_out(o, "row0", make(R)), cu_rows=_out(o, "cu_rows", make(R + 1)),
+               ctx_len=_out(o, "ctx_len", make(R)), batch=_out(o, "batch", make(1)),
+               free_count=_out(o, "free_count", make(1)), row_req=_out(o, "row_req", make(max_rows)),
+               row_pos=_out(o, "row_pos", make(max_rows)),
+               row_slot=_out(o, "row_slot", make(max_rows, torch.int64)),
+               row_token=None if x0 is None and tokens is None else _out(o, "row_token", make(max_rows)),
+               status=_out(o, "status", make(R)))
+    ws = workspace if workspace is not None else _workspace(sd_slot_reserve_workspace_size(R), dev)
+    n, m, one = (R,), (max_rows,), (1,)
+    code = lib().sd_slot_reserve(
+        _stream(stream), R, int(q_max), int(block_size), mb, free_list.numel(), max_rows, 1 if padded else 0,
+        _ptr_on(seq_len, torch.int64, "seq_len", dev), _ptr_on(ell, i32, "ell", dev, n),
+        _ptr_on(x0, i32, "x0", dev, n), _ptr_on(tokens, i32, "tokens", dev),
+        0 if tokens is None else tokens.shape[1], _ptr_on(block_table, i32, "block_table", dev, (R, mb)),
+        _ptr_on(free_list, i32, "free_list", dev), _ptr_on(free_count, i32, "free_count", dev, one),
+        _ptr_on(res["ell"], i32, "out ell", dev, n), _ptr_on(res["row0"], i32, "row0", dev, n),
+        _ptr_on(res["cu_rows"], i32, "cu_rows", dev, (R + 1,)), _ptr_on(res["ctx_len"], i32, "ctx_len", dev, n),
+        _ptr_on(res["batch"], i32, "batch", dev, one), _ptr_on(res["free_count"], i32, "out free_count", dev, one),
+        _ptr_on(res["row_req"], i32, "row_req", dev, m), _ptr_on(res["row_pos"], i32, "row_pos", dev, m),
+        _ptr_on(res["row_slot"], torch.int64, "row_slot", dev, m),
+        _ptr_on(res["row_token"], i32, "row_token", dev, m), _ptr_on(res["status"], i32, "status", dev, n),
+        _ptr_on(ws, torch.uint8, "workspace", dev), ws.numel())
+    _check("sd_slot_reserve", code)
+    return res
+
+
+def sd_slot_commit_workspace_size(R):
+    return lib().sd_slot_commit_workspace_size(R)
+
+
+@_on_device
+@_on_stream
+def sd_slot_commit(seq_len, ell, n_acc, block_table, free_list, free_count, block_size, q_max=None,
+                   out_tokens=None, x0=None, status=None, release=None, keep=None, out=None, workspace=None,
+                   *, stream=None):
+    """Keep what verification accepted of a step and give the other blocks
+    back.  seq_len [R] int64, ell [R] int32 and free_count [1] int32 as
+    sd_slot_reserve left them, n_acc, out_tokens [R][q_max], status sd_verify's,
+    x0 [R] int32 the step's anchors (with out_tokens: the next ones are
+    returned); release, keep [R] int32.  free_list is updated in place, and
+    status where a request is refused.  Returns a dict of device tensors:
+    seq_len, n_new, free_count, x0 (None without out_tokens)."""
+    dev = _device_of(seq_len, "seq_len")
+    R = seq_len.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be 2-D")
+    mb = block_table.shape[1]
+    if out_tokens is not None:
+        if out_tokens.dim() != 2 or q_max not in (None, out_tokens.shape[1]):
+            raise ValueError("out_tokens must be [R][q_max]")
+        q_max = out_tokens.shape[1]
+    elif q_max is None:
+        raise ValueError("q_max is needed without out_tokens")
+    o = out or {}
+    i32 = torch.int32
+    res = dict(seq_len=_out(o, "seq_len", lambda: torch.empty(R, dtype=torch.int64, device=dev)),
+               n_new=_out(o, "n_new", lambda: torch.empty(R, dtype=i32, device=dev)),
+               free_count=_out(o, "free_count", lambda: torch.empty(1, dtype=i32, device=dev)),
+               x0=None if out_tokens is None
+               else _out(o, "x0", lambda: torch.empty(R, dtype=i32, device=dev)))
+    ws = workspace if workspace is not None else _workspace(sd_slot_commit_workspace_size(R), dev)
+    n, one = (R,), (1,)
+    code = lib().sd_slot_commit(
+        _stream(stream), R, int(q_max), int(block_size), mb, free_list.numel(),
+        _ptr_on(seq_len, torch.int64, "seq_len", dev), _ptr_on(ell, i32, "ell", dev, n),
+        _ptr_on(n_acc, i32, "n_acc", dev, n),
+        None if out_tokens is None else _ptr_on(out_tokens, i32, "out_tokens", dev, (R, q_max)),
+        _ptr_on(x0, i32, "x0", dev, n), _ptr_on(release, i32, "release", dev, n), _ptr_on(keep, i32, "keep", dev, n),
+        _ptr_on(block_table, i32, "block_table", dev, (R, mb)), _ptr_on(free_list, i32, "free_list", dev),
+        _ptr_on(free_count, i32, "free_count", dev, one), _ptr_on(status, i32, "status", dev, n),
+        _ptr_on(res["seq_len"], torch.int64, "out seq_len", dev, n), _ptr_on(res["x0"], i32, "out x0", dev, n),
+        _ptr_on(res["n_new"], i32, "n_new", dev, n), _ptr_on(res["free_count"], i32, "out free_count", dev, one),
+        _ptr_on(ws, torch.uint8, "workspace", dev), ws.numel())
+    _check("sd_slot_commit", code)
+    return res

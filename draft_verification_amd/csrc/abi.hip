@@ -15,6 +15,8 @@ extern "C" const char* sd_status_string(int code) {
     case SD_ST_ZERO_Z: return "logit row is entirely -inf";
     case SD_ST_ZERO_RESIDUAL: return "rejection with empty residual: drawn from the target";
     case SD_ST_ZERO_Q: return "draft probability of the tested token is zero";
+    case SD_ST_BAD_INPUT: return "a request's device-side argument is out of range";
+    case SD_ST_NO_SLOT: return "fewer rows than asked for: no cache slots or rows left";
     default: return "unknown status";
   }
 }

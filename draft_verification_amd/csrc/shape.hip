@@ -1,0 +1,350 @@
+// sd_logit_shape and sd_token_counts: the target rows of a verification step
+// with the request's penalties, biases and grammar masks applied, and the
+// token counts behind the penalties.
+//
+// Verification is lossless with respect to the target rows it is given
+// (speculative-decoding history page, "1.1 mechanism"), so everything a
+// request asks of the target's distribution has to be in those rows before
+// sd_verify reads them.  Row i of a request scores the token after the drafts
+// x_1..x_i, so those drafts count as written there, although they are not in
+// the request's state until they are accepted.
+#include "sdv_host.h"
+#include "verify_common.h"
+
+namespace {
+
+constexpr int kShapeThreads = 256;
+constexpr int kVecTokens = 8;                              // tokens per thread: one mask byte
+constexpr int kShapeChunk = kShapeThreads * kVecTokens;    // tokens per workgroup
+
+struct ShapeArgs {
+  const char* logits;
+  char* out;
+  const int32_t* row0;
+  const int32_t* ell;
+  const int32_t* draft;
+  const float* rep;
+  const float* freq;
+  const float* pres;
+  const uint32_t* seen;
+  const int32_t* counts;
+  const int32_t* slot;
+  const int64_t* bias_off;
+  const int32_t* bias_tok;
+  const float* bias_val;
+  const uint32_t* mask;
+  const int32_t* mask_row0;
+  int32_t* status;
+  int64_t n_bias;
+  int64_t ld_bytes;
+  int gmax, V, n_ch, n_rows, n_slots, ld_seen, ld_counts, ld_mask, n_mask_rows;
+};
+
+// Eight consecutive logits as floats, and back with one rounding each.
+template <bool BF16>
+struct Oct;
+template <>
+struct Oct<true> {
+  static constexpr int kBytes = 16;
+  SDV_DEV static void load(const char* p, float* x) {
+    const uint4 v = *(const uint4*)p;
+    sdv::Vec<true>::unpack(v, x);
+  }
+  SDV_DEV static void store(char* p, const float* x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w[k] = (uint32_t)sdv::f32_to_bf16_rne(x[2 * k]) | ((uint32_t)sdv::f32_to_bf16_rne(x[2 * k + 1]) << 16);
+    *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Oct<false> {
+  static constexpr int kBytes = 32;
+  SDV_DEV static void load(const char* p, float* x) {
+    *(float4*)x = ((const float4*)p)[0];
+    *(float4*)(x + 4) = ((const float4*)p)[1];
+  }
+  SDV_DEV static void store(char* p, const float* x) {
+    ((float4*)p)[0] = *(const float4*)x;
+    ((float4*)p)[1] = *(const float4*)(x + 4);
+  }
+};
+
+// One workgroup per (request, chunk of 2048 tokens); a thread owns eight
+// consecutive tokens in every row of the request, so the request's state is
+// read once and stays in registers while the rows stream past.
+template <bool BF16>
+__global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
+  __shared__ int last[kShapeChunk];   // 1 + index of a token's last bias entry
+  const int r = blockIdx.x / a.n_ch, ch = blockIdx.x % a.n_ch;
+  const int tid = threadIdx.x;
+  const int n = min(a.ell[r], a.gmax) + 1;   // rows
+  if (n <= 0) {
+    if (ch == 0 && tid == 0) a.status[r] = 0;
+    return;
+  }
+  const int row0 = a.row0[r];
+  const float rep = a.rep ? a.rep[r] : 1.0f;
+  const float freq = a.freq ? a.freq[r] : 0.0f;
+  const float pres = a.pres ? a.pres[r] : 0.0f;
+  const int srow = a.slot ? a.slot[r] : r;
+  const int m0 = a.mask_row0 ? a.mask_row0[r] : -1;
+  const int64_t b0 = a.bias_off ? a.bias_off[r] : 0, b1 = a.bias_off ? a.bias_off[r + 1] : 0;
+  const float inf = __builtin_huge_valf();
+  const bool pen = rep != 1.0f || freq != 0.0f || pres != 0.0f;
+  bool ok = row0 >= 0 && (int64_t)row0 + n <= a.n_rows;
+  ok = ok && rep > 0.0f && rep < inf && fabsf(freq) < inf && fabsf(pres) < inf;
+  ok = ok && (!pen || (srow >= 0 && srow < a.n_slots));
+  ok = ok && (m0 < 0 || (int64_t)m0 + n <= a.n_mask_rows);
+  ok = ok && b0 >= 0 && b0 <= b1 && b1 <= a.n_bias;
+  if (!ok) {   // uniform over the request's workgroups: none of its rows is written
+    if (ch == 0 && tid == 0) a.status[r] = SD_ST_BAD_INPUT;
+    return;
+  }
+
+  const int v0 = ch * kShapeChunk + tid * kVecTokens;
+  const bool mine = v0 < a.V;
+  int bad = 0;
+  float bias[kVecTokens] = {};
+  unsigned biased = 0;
+  if (b1 > b0) {
+#pragma unroll
+    for (int e = 0; e < kVecTokens; ++e) last[e * kShapeThreads + tid] = 0;
+    __syncthreads();
+    const int nb = (int)(b1 - b0);
+    for (int i = tid; i < nb; i += kShapeThreads) {
+      const int t = a.bias_tok[b0 + i];
+      if (t < 0 || t >= a.V) bad = 1;
+      else if (t / kShapeChunk == ch) atomicMax(&last[t % kShapeChunk], i + 1);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kVecTokens; ++e) {
+      const int i = last[tid * kVecTokens + e];
+      if (i > 0) {
+        bias[e] = a.bias_val[b0 + i - 1];
+        biased |= 1u << e;
+      }
+    }
+  }
+  const int32_t* draft = a.draft ? a.draft + (int64_t)r * a.gmax : nullptr;
+  if (ch == 0) {   // the request's status
+    if (pen && draft)
+      for (int i = tid; i < n - 1; i += kShapeThreads) bad |= draft[i] < 0 || draft[i] >= a.V;
+    bad = __syncthreads_or(bad);
+    if (tid == 0) a.status[r] = bad ? SD_ST_BAD_TOKEN : 0;
+  }
+  if (!mine) return;
+
+  unsigned seen = 0;
+  float c[kVecTokens] = {};
+  if (pen && a.seen) {
+    seen = ((const uint8_t*)(a.seen + (int64_t)srow * a.ld_seen))[v0 >> 3];
+    if (seen && a.counts) {
+      const int4* p = (const int4*)(a.counts + (int64_t)srow * a.ld_counts + v0);
+      const int4 p0 = p[0], p1 = p[1];
+      const int k[kVecTokens] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+      for (int e = 0; e < kVecTokens; ++e) c[e] = (seen >> e) & 1 ? (float)k[e] : 0.0f;
+    }
+  }
+  const char* src = a.logits + (int64_t)row0 * a.ld_bytes + (int64_t)v0 * (Oct<BF16>::kBytes / kVecTokens);
+  char* dst = a.out + (src - a.logits);
+  const uint8_t* mask = m0 >= 0 ? (const uint8_t*)(a.mask + (int64_t)m0 * a.ld_mask) + (v0 >> 3) : nullptr;
+  const bool copy = a.out != a.logits;
+  for (int i = 0; i < n; ++i) {
+    if (i > 0 && pen && draft) {
+      const int x = draft[i - 1];
+#pragma unroll
+      for (int e = 0; e < kVecTokens; ++e)
+        if (x == v0 + e) {
+          c[e] += 1.0f;
+          seen |= 1u << e;
+        }
+    }
+    const unsigned allowed = mask ? mask[(int64_t)i * a.ld_mask * 4] : 0xFFu;
+    const unsigned touched = seen | biased | (allowed ^ 0xFFu);
+    if (copy || touched) {
+      float x[kVecTokens];
+      Oct<BF16>::load(src, x);
+#pragma unroll
+      for (int e = 0; e < kVecTokens; ++e) {
+        if ((seen >> e) & 1) {
+          x[e] = x[e] > 0.0f ? x[e] / rep : x[e] * rep;
+          x[e] -= freq * c[e];
+          if (c[e] > 0.0f) x[e] -= pres;
+        }
+        if ((biased >> e) & 1) x[e] += bias[e];
+        if (!((allowed >> e) & 1)) x[e] = -inf;
+      }
+      Oct<BF16>::store(dst, x);
+    }
+    src += a.ld_bytes;
+    dst += a.ld_bytes;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Token counts.
+
+struct CountArgs {
+  const int32_t* tokens;
+  const int64_t* start;
+  const int32_t* length;
+  const int32_t* prompt_len;
+  const int32_t* slot;
+  const int32_t* reset;
+  uint32_t* seen;
+  int32_t* counts;
+  int32_t* status;
+  int64_t n_tokens;
+  int V, width, n_slots, ld_seen, ld_counts;
+};
+
+// The request's tokens and state row; false where they are out of range.
+SDV_DEV bool count_row(const CountArgs& a, int r, int64_t* at, int* n, int* srow) {
+  *at = a.start ? a.start[r] : (int64_t)r * a.width;
+  *n = a.length ? a.length[r] : a.width;
+  *srow = a.slot ? a.slot[r] : r;
+  if (*n < 0) *n = 0;
+  return *srow >= 0 && *srow < a.n_slots && *at >= 0 && *at <= a.n_tokens && *n <= a.n_tokens - *at;
+}
+
+constexpr int kCountThreads = 256;
+
+__global__ __launch_bounds__(kCountThreads) void k_count_clear(CountArgs a) {
+  const int r = blockIdx.x;
+  int64_t at;
+  int n, srow;
+  const bool ok = count_row(a, r, &at, &n, &srow);
+  const int first = blockIdx.y * kCountThreads + threadIdx.x, step = gridDim.y * kCountThreads;
+  if (first == 0) a.status[r] = ok ? 0 : SD_ST_BAD_INPUT;
+  if (!ok || !a.reset || !a.reset[r]) return;
+  for (int w = first; w < (a.V + 31) / 32; w += step) a.seen[(int64_t)srow * a.ld_seen + w] = 0;
+  if (a.counts)
+    for (int v = first; v < a.V; v += step) a.counts[(int64_t)srow * a.ld_counts + v] = 0;
+}
+
+__global__ __launch_bounds__(kCountThreads) void k_count_add(CountArgs a) {
+  const int r = blockIdx.x;
+  int64_t at;
+  int n, srow;
+  if (!count_row(a, r, &at, &n, &srow)) return;
+  const int prompt = a.prompt_len ? a.prompt_len[r] : 0;
+  uint32_t* seen = a.seen + (int64_t)srow * a.ld_seen;
+  int32_t* counts = a.counts ? a.counts + (int64_t)srow * a.ld_counts : nullptr;
+  const int step = gridDim.y * kCountThreads;
+  for (int64_t i = blockIdx.y * kCountThreads + threadIdx.x; i < n; i += step) {
+    const int t = a.tokens[at + i];
+    if (t < 0 || t >= a.V) continue;
+    atomicOr(&seen[t >> 5], 1u << (t & 31));
+    if (counts && i >= prompt) atomicAdd(&counts[t], 1);
+  }
+}
+
+}  // namespace
+
+extern "C" int sd_logit_shape(hipStream_t stream, int R, int gamma_max, int V, int ld, int dtype,
+                              const void* logits, void* out, int n_rows, const int32_t* row0,
+                              const int32_t* ell, const int32_t* draft_tokens, const float* repetition,
+                              const float* frequency, const float* presence, const uint32_t* seen,
+                              int ld_seen, const int32_t* counts, int ld_counts, int n_slots,
+                              const int32_t* slot, const int64_t* bias_off, const int32_t* bias_tok,
+                              const float* bias_val, long long n_bias, const uint32_t* mask, int ld_mask,
+                              int n_mask_rows, const int32_t* mask_row0, int32_t* status) {
+  if (R < 0 || gamma_max < 0 || V < 8 || (V % 8) != 0 || ld < V || (ld % 8) != 0 || n_rows < 0)
+    return SD_EINVAL;
+  if (gamma_max > SD_MAX_GAMMA || V > SD_MAX_VOCAB) return SD_EUNSUPPORTED;
+  if (dtype != SD_DTYPE_F32 && dtype != SD_DTYPE_BF16) return SD_EINVAL;
+  if (R == 0) return SD_OK;
+  if (!logits || !out || !row0 || !ell || !status) return SD_EINVAL;
+  if ((((uintptr_t)logits) & 15) != 0 || (((uintptr_t)out) & 15) != 0) return SD_EINVAL;
+  const int words = (V + 31) / 32;
+  const bool pen = repetition || frequency || presence;
+  if (pen && !seen) return SD_EINVAL;
+  if ((frequency || presence) && !counts) return SD_EINVAL;
+  if (pen && (n_slots < 1 || ld_seen < words)) return SD_EINVAL;
+  if (counts && (ld_counts < V || (ld_counts % 4) != 0 || (((uintptr_t)counts) & 15) != 0)) return SD_EINVAL;
+  if (bias_off && (n_bias < 0 || (n_bias > 0 && (!bias_tok || !bias_val)))) return SD_EINVAL;
+  if (bias_off && n_bias > 0x7FFFFFFFLL) return SD_EUNSUPPORTED;
+  if (mask && !mask_row0) return SD_EINVAL;
+  if (mask_row0 && (n_mask_rows < 0 || (n_mask_rows > 0 && (!mask || ld_mask < words)))) return SD_EINVAL;
+  ShapeArgs a;
+  a.logits = (const char*)logits;
+  a.out = (char*)out;
+  a.row0 = row0;
+  a.ell = ell;
+  a.draft = draft_tokens;
+  a.rep = repetition;
+  a.freq = frequency;
+  a.pres = presence;
+  a.seen = seen;
+  a.counts = counts;
+  a.slot = slot;
+  a.bias_off = bias_off;
+  a.bias_tok = bias_tok;
+  a.bias_val = bias_val;
+  a.mask = mask;
+  a.mask_row0 = mask_row0;
+  a.status = status;
+  a.n_bias = bias_off ? n_bias : 0;
+  a.ld_bytes = (int64_t)ld * (dtype == SD_DTYPE_BF16 ? 2 : 4);
+  a.gmax = gamma_max;
+  a.V = V;
+  a.n_ch = (V + kShapeChunk - 1) / kShapeChunk;
+  a.n_rows = n_rows;
+  a.n_slots = n_slots;
+  a.ld_seen = ld_seen;
+  a.ld_counts = ld_counts;
+  a.ld_mask = ld_mask;
+  a.n_mask_rows = n_mask_rows;
+  const long long items = (long long)R * a.n_ch;
+  if (items > 0xFFFFFFFFLL / kShapeThreads) return SD_EUNSUPPORTED;  // work-items of one launch
+  const dim3 g((unsigned)items), b(kShapeThreads);
+  if (dtype == SD_DTYPE_BF16)
+    SDV_TRY_LAUNCH(sdv::launch(k_logit_shape<true>, g, b, 0, stream, a));
+  else
+    SDV_TRY_LAUNCH(sdv::launch(k_logit_shape<false>, g, b, 0, stream, a));
+  return SD_OK;
+}
+
+extern "C" int sd_token_counts(hipStream_t stream, int R, int V, const int32_t* tokens, long long n_tokens,
+                               int width, const int64_t* start, const int32_t* length,
+                               const int32_t* prompt_len, const int32_t* slot, const int32_t* reset,
+                               uint32_t* seen, int ld_seen, int32_t* counts, int ld_counts, int n_slots,
+                               int32_t* status) {
+  if (R < 0 || V < 8 || (V % 8) != 0 || n_tokens < 0 || width < 0) return SD_EINVAL;
+  if (V > SD_MAX_VOCAB) return SD_EUNSUPPORTED;
+  if (R == 0) return SD_OK;
+  if (!seen || !status || n_slots < 1 || ld_seen < (V + 31) / 32) return SD_EINVAL;
+  if (n_tokens > 0 && !tokens) return SD_EINVAL;
+  if (counts && (ld_counts < V || (ld_counts % 4) != 0 || (((uintptr_t)counts) & 15) != 0)) return SD_EINVAL;
+  if (start && !length) return SD_EINVAL;
+  if (!start && (long long)R * width > n_tokens) return SD_ERANGE;
+  if ((long long)R * kCountThreads > 0xFFFFFFFFLL) return SD_EUNSUPPORTED;
+  CountArgs a;
+  a.tokens = tokens;
+  a.start = start;
+  a.length = length;
+  a.prompt_len = prompt_len;
+  a.slot = slot;
+  a.reset = reset;
+  a.seen = seen;
+  a.counts = counts;
+  a.status = status;
+  a.n_tokens = n_tokens;
+  a.V = V;
+  a.width = width;
+  a.n_slots = n_slots;
+  a.ld_seen = ld_seen;
+  a.ld_counts = ld_counts;
+  const long long most = start ? n_tokens : width;
+  auto split = [&](long long work) {   // workgroups per request
+    const long long fill = (2048 + R - 1) / R, need = (work + kCountThreads - 1) / kCountThreads;
+    return (unsigned)(need < 1 ? 1 : (need < fill ? need : fill));
+  };
+  SDV_TRY_LAUNCH(sdv::launch(k_count_clear, dim3(R, reset ? split(V) : 1), dim3(kCountThreads), 0, stream, a));
+  SDV_TRY_LAUNCH(sdv::launch(k_count_add, dim3(R, split(most)), dim3(kCountThreads), 0, stream, a));
+  return SD_OK;
+}

@@ -10,8 +10,11 @@
  *   sd_markov_draft  the low-rank Markov drafting head and the confidence head
  *
  * and around them: sd_rnn_draft (the RNN form of the drafting head), the
- * budget planner (sd_lightspec_update, sd_lightspec_plan) and sd_uniforms
- * (the uniforms behind the random decisions).
+ * budget planner (sd_lightspec_update, sd_lightspec_plan), sd_uniforms
+ * (the uniforms behind the random decisions), sd_slot_reserve and
+ * sd_slot_commit (the verify batch's rows and paged cache slots),
+ * sd_logit_shape and sd_token_counts (penalties, biases and grammar masks on
+ * the target rows, and the token counts behind them).
  *
  * Sources, by page and section:
  *   [DS]  "DSpark: Confidence-Scheduled Speculative Decoding with
@@ -89,6 +92,8 @@ extern "C" {
 #define SD_ST_ZERO_Z         4   /* a needed logit row is entirely -inf */
 #define SD_ST_ZERO_RESIDUAL  8   /* rejection with no residual mass: drawn from p */
 #define SD_ST_ZERO_Q        16   /* q(x) = 0 at a tested draft token */
+#define SD_ST_BAD_INPUT     32   /* a request's device-side argument is out of range */
+#define SD_ST_NO_SLOT       64   /* sd_slot_reserve: fewer rows than asked for */
 
 /* build limits */
 #define SD_MAX_GAMMA           255     /* draft positions per request */
@@ -409,6 +414,163 @@ int sd_lightspec_plan(hipStream_t stream, int R, int gamma_max, const double* em
  */
 int sd_uniforms(hipStream_t stream, uint64_t seed, long long n, const int64_t* req,
                 const int64_t* pos, int draw, float* out);
+
+/*
+ * sd_logit_shape - penalties, biases and grammar masks on the rows of a
+ * verify batch, before sd_verify reads them.  Verification reproduces the
+ * distribution of the target rows it is given [SD 1.1], so what a request
+ * asks of its output is applied to those rows.
+ *
+ * Row i of request r, i = 0..ell[r], is row0[r] + i (sd_verify's target row
+ * of position i + 1); it scores the token after the drafts x_1..x_i,
+ * x_i = draft_tokens[r][i-1], which count as written there.  With
+ *   s(v)  the bit of token v in seen[slot[r]], or v among x_1..x_i
+ *   n(v)  counts[slot[r]][v] (0 where the bit is clear) plus v's occurrences
+ *         among x_1..x_i
+ * a logit l(v) becomes, in fp32 and rounded once to the rows' type,
+ *   1. where s(v):  l > 0 ? l / repetition[r] : l * repetition[r]
+ *   2. where s(v):  l - frequency[r] * n(v), and where n(v) > 0: - presence[r]
+ *   3. l + b(v), where the request's bias list has v (its last entry counts)
+ *   4. -inf where the row's mask bit of v is 0, whatever l is
+ * A token that no term touches keeps its value.
+ *
+ *   R, gamma_max, V, ld, dtype as sd_verify; ell < 0: the request has no rows
+ *   logits, out  [n_rows][ld], 16-byte aligned; out may be logits (only the
+ *                touched parts of a row are then read and written), else the
+ *                two do not overlap and rows outside the batch and entries
+ *                past V are left as they are in out
+ *   draft_tokens [R][gamma_max] int32, or NULL: no draft counts as written
+ *   repetition (finite, > 0), frequency, presence (finite)  [R] fp32, each
+ *                NULL for 1, 0 and 0
+ *   seen         [n_slots][ld_seen] 32-bit words, bit v % 32 of word v / 32
+ *                is token v; ld_seen >= ceil(V / 32); required with penalties
+ *   counts       [n_slots][ld_counts] int32, >= 0, ld_counts >= V and a
+ *                multiple of 4, 16-byte aligned; required with frequency or
+ *                presence
+ *   slot         [R] int32 state row of each request, or NULL: r
+ *   bias_off     [R + 1] int64 or NULL: request r's entries are
+ *                bias_off[r]..bias_off[r+1]-1 of bias_tok, bias_val [n_bias]
+ *   mask         [n_mask_rows][ld_mask] 32-bit words in seen's layout, or
+ *                NULL; row i of request r uses row mask_row0[r] + i, and a
+ *                request with mask_row0[r] < 0 has no mask
+ *   status       [R] int32 out: BAD_TOKEN where a bias entry, or (with
+ *                penalties) a draft among x_1..x_ell, lies outside [0, V):
+ *                it is skipped; BAD_INPUT where a row, slot, mask row, bias
+ *                offset or penalty is out of range: none of the request's
+ *                rows is written
+ */
+int sd_logit_shape(hipStream_t stream, int R, int gamma_max, int V, int ld, int dtype,
+                   const void* logits, void* out, int n_rows, const int32_t* row0,
+                   const int32_t* ell, const int32_t* draft_tokens, const float* repetition,
+                   const float* frequency, const float* presence, const uint32_t* seen,
+                   int ld_seen, const int32_t* counts, int ld_counts, int n_slots,
+                   const int32_t* slot, const int64_t* bias_off, const int32_t* bias_tok,
+                   const float* bias_val, long long n_bias, const uint32_t* mask, int ld_mask,
+                   int n_mask_rows, const int32_t* mask_row0, int32_t* status);
+
+/*
+ * sd_token_counts - the state behind the penalties: for every token t of
+ * request r's list, in [0, V) (others, such as sd_verify's -1 padding, are
+ * skipped), the bit of t in seen[slot[r]] is set, and for those past the
+ * first prompt_len[r] counts[slot[r]][t] grows by one.
+ *   tokens [n_tokens] int32; request r's list is tokens[start[r]] ..
+ *   tokens[start[r] + length[r] - 1]; start NULL: r * width, length NULL
+ *   (only without start): width; a negative length is 0.  sd_verify's
+ *   out_tokens are a list of width gamma_max + 1.
+ *   prompt_len [R] int32 or NULL (0): prompt tokens are seen, not counted
+ *   reset      [R] int32 or NULL: where not 0 the state row is cleared first
+ *              (whatever it held)
+ *   seen, counts (or NULL), their leading dimensions, n_slots, slot as
+ *   sd_logit_shape; requests may share a state row
+ *   status [R] int32 out: BAD_INPUT where the list or the slot is out of
+ *   range (the request is left out)
+ */
+int sd_token_counts(hipStream_t stream, int R, int V, const int32_t* tokens, long long n_tokens,
+                    int width, const int64_t* start, const int32_t* length,
+                    const int32_t* prompt_len, const int32_t* slot, const int32_t* reset,
+                    uint32_t* seen, int ld_seen, int32_t* counts, int ld_counts, int n_slots,
+                    int32_t* status);
+
+/*
+ * Rows and paged cache slots of a step [LS: token slots reserved and cut
+ * after the fact; DS 2.2: the batch is known on the device only].
+ *
+ * Request r has seq_len[r] tokens in the cache, at positions 0..seq_len-1;
+ * position p lives in block block_table[r][p / block_size], at offset
+ * p % block_size.  Between steps a request holds exactly
+ * ceil(seq_len / block_size) blocks; the other blocks of the pool are
+ * free_list[0..free_count-1].
+ *
+ * sd_slot_reserve - a step gives request r asked = min(ell[r], q_max-1) + 1
+ * rows (the anchor and ell drafts: sd_verify's target rows; a piece of a
+ * prompt), none where ell[r] < 0, at positions seq_len[r] onwards.  In the
+ * order of the requests, each gets as many of them as the table's width, the
+ * row buffers (packed rows) and the free blocks left by the requests before
+ * it allow; block number k of the step is free_list[free_count - 1 - k].
+ *   rows: packed (padded = 0): request after request, max_rows >= 1; padded:
+ *   request r owns rows r * q_max .., max_rows >= R * q_max else SD_ERANGE
+ *   n_blocks   blocks in the pool (the length of free_list; ids below it)
+ *   x0, tokens [R], [R][ld_tokens] int32: the rows' tokens.  With x0, row 0
+ *              of a request is x0[r] and row i tokens[r][i-1] (the anchor and
+ *              the drafts); without, row i is tokens[r][i].  Used only when
+ *              row_token is given
+ *   block_table [R][max_blocks] int32: the new blocks are entered, the other
+ *              entries left as they are
+ * Outputs:
+ *   ell_out    [R] int32: rows - 1, what is scheduled now (-1: no rows)
+ *   row0       [R] int32 first row (sd_verify's tgt_row0); of a request
+ *              without rows some row inside the buffers
+ *   cu_rows    [R + 1] int32 exclusive prefix sums of the rows
+ *   ctx_len    [R] int32 seq_len + rows; batch [1] all rows; free_left [1]
+ *   row_req, row_pos [max_rows] int32, row_slot [max_rows] int64
+ *              (block * block_size + offset), row_token [max_rows] int32 or
+ *              NULL; -1 for every row that is no request's
+ *   status     [R] int32: NO_SLOT where a request got fewer rows than asked;
+ *              BAD_INPUT where seq_len is negative or past the table (no
+ *              rows, ctx_len 0) or a block id is outside [0, n_blocks) (its
+ *              rows have slot -1)
+ * ell_out may be ell and free_left may be free_count; seq_len is not changed,
+ * so a step that is not committed is repeated by passing the old free_count.
+ *
+ * sd_slot_commit - after verification: n_new[r] = 1 + min(n_accepted[r],
+ * ell[r]) tokens of the step stay (0 where ell[r] < 0 or status[r] has
+ * NONFINITE or ZERO_Z: the step is repeated), seq_len grows by n_new, and the
+ * blocks past the new length go back, request after request, to
+ * free_list[free_count..].  Where release[r] is not 0 (a finished request)
+ * seq_len becomes 0 and all its blocks go back, but for the first keep[r]
+ * (shared with others).
+ *   ell        [R] sd_slot_reserve's ell_out;  free_count: its free_left
+ *   n_accepted [R], out_tokens [R][q_max] sd_verify's (q_max = gamma_max + 1)
+ *   release, keep  [R] int32 or NULL
+ *   status     [R] int32 or NULL, sd_verify's; BAD_INPUT is added where
+ *              seq_len or ell is out of range (the request stays as it is)
+ *              or more blocks come back than the pool holds (dropped)
+ *   seq_len_out [R] int64 (usable as pos0 of the random decisions), n_new
+ *   [R] int32, free_count_out [1]; x0_out [R] int32 or NULL: the next anchors
+ *   out_tokens[r][n_accepted[r]] (x0[r] where n_new is 0).  seq_len_out,
+ *   x0_out and free_count_out may be seq_len, x0 and free_count.  The entries
+ *   of block_table stay as they are.
+ *
+ * block_size * max_blocks, R * q_max, R * max_blocks and max_rows stay below
+ * 2^31 - 256; workspaces of sd_slot_*_workspace_size(R) bytes.
+ */
+size_t sd_slot_reserve_workspace_size(int R);
+int sd_slot_reserve(hipStream_t stream, int R, int q_max, int block_size, int max_blocks,
+                    int n_blocks, int max_rows, int padded, const int64_t* seq_len,
+                    const int32_t* ell, const int32_t* x0, const int32_t* tokens, int ld_tokens,
+                    int32_t* block_table, const int32_t* free_list, const int32_t* free_count,
+                    int32_t* ell_out, int32_t* row0, int32_t* cu_rows, int32_t* ctx_len,
+                    int32_t* batch, int32_t* free_left, int32_t* row_req, int32_t* row_pos,
+                    int64_t* row_slot, int32_t* row_token, int32_t* status, void* workspace,
+                    size_t workspace_bytes);
+size_t sd_slot_commit_workspace_size(int R);
+int sd_slot_commit(hipStream_t stream, int R, int q_max, int block_size, int max_blocks,
+                   int n_blocks, const int64_t* seq_len, const int32_t* ell,
+                   const int32_t* n_accepted, const int32_t* out_tokens, const int32_t* x0,
+                   const int32_t* release, const int32_t* keep, const int32_t* block_table,
+                   int32_t* free_list, const int32_t* free_count, int32_t* status,
+                   int64_t* seq_len_out, int32_t* x0_out, int32_t* n_new, int32_t* free_count_out,
+                   void* workspace, size_t workspace_bytes);
 
 #ifdef __cplusplus
 }

@@ -27,4 +27,4 @@ Sources (cited by page title and section):
 Parity status per function is stated in each module header.
 """
 
-from . import rng, schedule, verify, markov, bf16, lightspec, rnn  # noqa: F401
+from . import rng, schedule, verify, markov, bf16, lightspec, rnn, shape, slots  # noqa: F401
