@@ -13,9 +13,11 @@
 
 namespace {
 
-constexpr int kShapeThreads = 256;
+constexpr int kShapeThreads = 64;
 constexpr int kVecTokens = 8;                              // tokens per thread: one mask byte
 constexpr int kShapeChunk = kShapeThreads * kVecTokens;    // tokens per workgroup
+constexpr long long kFullWaves = 8192;   // resident waves of the chip at this kernel's registers
+constexpr double kCacheBytes = 128 << 20;
 
 struct ShapeArgs {
   const char* logits;
@@ -38,52 +40,85 @@ struct ShapeArgs {
   int64_t n_bias;
   int64_t ld_bytes;
   int gmax, V, n_ch, n_rows, n_slots, ld_seen, ld_counts, ld_mask, n_mask_rows;
+  int group;   // rows of a request per workgroup
 };
 
-// Eight consecutive logits as floats, and back with one rounding each.
+// Eight consecutive logits as they lie in memory; a value is changed in its
+// place, so the others keep their bits.
 template <bool BF16>
 struct Oct;
 template <>
 struct Oct<true> {
   static constexpr int kBytes = 16;
-  SDV_DEV static void load(const char* p, float* x) {
-    const uint4 v = *(const uint4*)p;
-    sdv::Vec<true>::unpack(v, x);
+  uint4 q;
+  template <bool NT>
+  SDV_DEV void load(const char* p) { q = NT ? sdv::ld_nt(p) : *(const uint4*)p; }
+  template <bool NT>
+  SDV_DEV void store(char* p) const {
+    if (NT) sdv::st_nt(p, q);
+    else *(uint4*)p = q;
   }
-  SDV_DEV static void store(char* p, const float* x) {
-    uint32_t w[4];
+  SDV_DEV uint32_t& word(int k) { return k == 0 ? q.x : (k == 1 ? q.y : (k == 2 ? q.z : q.w)); }
+  SDV_DEV float get(int e) { return e & 1 ? sdv::bf16hi(word(e >> 1)) : sdv::bf16lo(word(e >> 1)); }
+  SDV_DEV void set(int e, float x) {
+    const uint32_t h = sdv::f32_to_bf16_rne(x);
+    uint32_t& w = word(e >> 1);
+    w = e & 1 ? (w & 0xFFFFu) | (h << 16) : (w & 0xFFFF0000u) | h;
+  }
+  // -inf wherever the bit of `allowed` is 0
+  SDV_DEV void keep(unsigned allowed) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      w[k] = (uint32_t)sdv::f32_to_bf16_rne(x[2 * k]) | ((uint32_t)sdv::f32_to_bf16_rne(x[2 * k + 1]) << 16);
-    *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int k = 0; k < 4; ++k) {
+      const unsigned two = allowed >> (2 * k);
+      const uint32_t m = ((two & 1u) ? 0xFFFFu : 0u) | ((two & 2u) ? 0xFFFF0000u : 0u);
+      uint32_t& w = word(k);
+      w = (w & m) | (0xFF80FF80u & ~m);
+    }
   }
 };
 template <>
 struct Oct<false> {
   static constexpr int kBytes = 32;
-  SDV_DEV static void load(const char* p, float* x) {
-    *(float4*)x = ((const float4*)p)[0];
-    *(float4*)(x + 4) = ((const float4*)p)[1];
+  uint4 q[2];
+  template <bool NT>
+  SDV_DEV void load(const char* p) {
+    q[0] = NT ? sdv::ld_nt(p) : ((const uint4*)p)[0];
+    q[1] = NT ? sdv::ld_nt(p + 16) : ((const uint4*)p)[1];
   }
-  SDV_DEV static void store(char* p, const float* x) {
-    ((float4*)p)[0] = *(const float4*)x;
-    ((float4*)p)[1] = *(const float4*)(x + 4);
+  template <bool NT>
+  SDV_DEV void store(char* p) const {
+    if (NT) {
+      sdv::st_nt(p, q[0]);
+      sdv::st_nt(p + 16, q[1]);
+    } else {
+      ((uint4*)p)[0] = q[0];
+      ((uint4*)p)[1] = q[1];
+    }
+  }
+  SDV_DEV uint32_t& word(int e) {
+    uint4& v = q[e >> 2];
+    return (e & 3) == 0 ? v.x : ((e & 3) == 1 ? v.y : ((e & 3) == 2 ? v.z : v.w));
+  }
+  SDV_DEV float get(int e) { return __uint_as_float(word(e)); }
+  SDV_DEV void set(int e, float x) { word(e) = __float_as_uint(x); }
+  SDV_DEV void keep(unsigned allowed) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) word(e) = (allowed >> e) & 1u ? word(e) : 0xFF800000u;
   }
 };
 
-// One workgroup per (request, chunk of 2048 tokens); a thread owns eight
-// consecutive tokens in every row of the request, so the request's state is
-// read once and stays in registers while the rows stream past.
-template <bool BF16>
+// One wave per (request, chunk of 512 tokens, group of rows); a lane owns
+// eight consecutive tokens in every row of the group, so the request's state
+// is read once and stays in registers while the rows stream past.  NT: a
+// batch that does not fit the last-level cache.
+template <bool BF16, bool NT>
 __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
+  constexpr int kRows = NT ? 2 : 1;   // rows whose loads are issued together
   __shared__ int last[kShapeChunk];   // 1 + index of a token's last bias entry
   const int r = blockIdx.x / a.n_ch, ch = blockIdx.x % a.n_ch;
   const int tid = threadIdx.x;
+  // everything that describes the request is requested together
   const int n = min(a.ell[r], a.gmax) + 1;   // rows
-  if (n <= 0) {
-    if (ch == 0 && tid == 0) a.status[r] = 0;
-    return;
-  }
   const int row0 = a.row0[r];
   const float rep = a.rep ? a.rep[r] : 1.0f;
   const float freq = a.freq ? a.freq[r] : 0.0f;
@@ -91,6 +126,12 @@ __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
   const int srow = a.slot ? a.slot[r] : r;
   const int m0 = a.mask_row0 ? a.mask_row0[r] : -1;
   const int64_t b0 = a.bias_off ? a.bias_off[r] : 0, b1 = a.bias_off ? a.bias_off[r + 1] : 0;
+  const int i0 = blockIdx.y * a.group, i1 = min(n, i0 + a.group);
+  const bool tell = ch == 0 && i0 == 0;      // this wave reports the request's status
+  if (i0 >= i1) {
+    if (tell && tid == 0) a.status[r] = 0;
+    return;
+  }
   const float inf = __builtin_huge_valf();
   const bool pen = rep != 1.0f || freq != 0.0f || pres != 0.0f;
   bool ok = row0 >= 0 && (int64_t)row0 + n <= a.n_rows;
@@ -98,13 +139,41 @@ __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
   ok = ok && (!pen || (srow >= 0 && srow < a.n_slots));
   ok = ok && (m0 < 0 || (int64_t)m0 + n <= a.n_mask_rows);
   ok = ok && b0 >= 0 && b0 <= b1 && b1 <= a.n_bias;
-  if (!ok) {   // uniform over the request's workgroups: none of its rows is written
-    if (ch == 0 && tid == 0) a.status[r] = SD_ST_BAD_INPUT;
+  if (!ok) {   // uniform over the request's waves: none of its rows is written
+    if (tell && tid == 0) a.status[r] = SD_ST_BAD_INPUT;
     return;
   }
 
   const int v0 = ch * kShapeChunk + tid * kVecTokens;
   const bool mine = v0 < a.V;
+  const int m_all = mine ? i1 - i0 : 0;   // rows of this lane
+  const char* src = a.logits + ((int64_t)row0 + i0) * a.ld_bytes + (int64_t)v0 * (Oct<BF16>::kBytes / kVecTokens);
+  char* dst = a.out + (src - a.logits);
+  const int64_t mask_step = (int64_t)a.ld_mask * 4;
+  const uint8_t* mask =
+      m0 >= 0 ? (const uint8_t*)(a.mask + ((int64_t)m0 + i0) * a.ld_mask) + (v0 >> 3) : nullptr;
+  const bool copy = a.out != a.logits;
+  unsigned allowed[kRows];
+  Oct<BF16> x[kRows];
+  // A large batch is bound by bytes: a row's logits wait for its mask, and
+  // what is neither read nor kept is not loaded.  A small one is bound by the
+  // chain of loads: the first rows are requested here, with the state.
+  auto fetch_mask = [&](int i) {
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) allowed[k] = mask && i + k < m_all ? mask[(i + k) * mask_step] : 0xFFu;
+  };
+  auto fetch_all = [&](int i) {
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      if (i + k < m_all) x[k].template load<NT>(src + (i + k) * a.ld_bytes);
+  };
+  if (!NT) {
+    fetch_mask(0);
+    fetch_all(0);
+  }
+  unsigned seen = 0;
+  if (pen && a.seen && mine) seen = ((const uint8_t*)(a.seen + (int64_t)srow * a.ld_seen))[v0 >> 3];
+
   int bad = 0;
   float bias[kVecTokens] = {};
   unsigned biased = 0;
@@ -128,60 +197,77 @@ __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
       }
     }
   }
-  const int32_t* draft = a.draft ? a.draft + (int64_t)r * a.gmax : nullptr;
-  if (ch == 0) {   // the request's status
-    if (pen && draft)
+  float c[kVecTokens] = {};   // counts up to 2^24 are exact
+  if (seen && a.counts) {
+    const int4* p = (const int4*)(a.counts + (int64_t)srow * a.ld_counts + v0);
+    const int4 p0 = p[0], p1 = p[1];
+    const int k[kVecTokens] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+    for (int e = 0; e < kVecTokens; ++e) c[e] = (seen >> e) & 1 ? (float)k[e] : 0.0f;
+  }
+  // a draft before the row counts as written
+  const int32_t* draft = pen && a.draft ? a.draft + (int64_t)r * a.gmax : nullptr;
+  auto count = [&](int t) {
+#pragma unroll
+    for (int e = 0; e < kVecTokens; ++e)
+      if (t == v0 + e) {
+        c[e] += 1.0f;
+        seen |= 1u << e;
+      }
+  };
+  if (draft)
+    for (int i = 0; i < i0; ++i) count(draft[i]);
+
+  for (int i = 0; i < m_all; i += kRows) {
+    if (NT) fetch_mask(i);
+    // the tokens met before each row; the draft before it is new in it
+    unsigned met[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      met[k] = k ? met[k - 1] : seen;
+      if (draft && i + k > 0 && i + k < m_all) {
+        const int t = draft[i0 + i + k - 1];
+        if ((t >> 3) == (v0 >> 3)) met[k] |= 1u << (t & 7);
+      }
+    }
+    if (NT) {
+#pragma unroll
+      for (int k = 0; k < kRows; ++k)
+        if (i + k < m_all && allowed[k] != 0 && (copy || (met[k] | biased | (allowed[k] ^ 0xFFu))))
+          x[k].template load<NT>(src + (i + k) * a.ld_bytes);
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (i + k >= m_all) break;
+      if (draft && i + k > 0 && met[k]) count(draft[i0 + i + k - 1]);
+      const unsigned hit = (met[k] | biased) & allowed[k];
+      if (hit) {
+#pragma unroll
+        for (int e = 0; e < kVecTokens; ++e)
+          if ((hit >> e) & 1) {
+            float y = x[k].get(e);
+            if ((met[k] >> e) & 1) {
+              y = y > 0.0f ? y / rep : y * rep;
+              y -= freq * c[e];
+              if (c[e] > 0.0f) y -= pres;
+            }
+            if ((biased >> e) & 1) y += bias[e];
+            x[k].set(e, y);
+          }
+      }
+      if (allowed[k] != 0xFFu) x[k].keep(allowed[k]);
+      if (copy || hit || allowed[k] != 0xFFu) x[k].template store<NT>(dst + (i + k) * a.ld_bytes);
+    }
+    if (!NT) {
+      fetch_mask(i + kRows);
+      fetch_all(i + kRows);
+    }
+  }
+  if (tell) {
+    if (draft)
       for (int i = tid; i < n - 1; i += kShapeThreads) bad |= draft[i] < 0 || draft[i] >= a.V;
     bad = __syncthreads_or(bad);
     if (tid == 0) a.status[r] = bad ? SD_ST_BAD_TOKEN : 0;
-  }
-  if (!mine) return;
-
-  unsigned seen = 0;
-  float c[kVecTokens] = {};
-  if (pen && a.seen) {
-    seen = ((const uint8_t*)(a.seen + (int64_t)srow * a.ld_seen))[v0 >> 3];
-    if (seen && a.counts) {
-      const int4* p = (const int4*)(a.counts + (int64_t)srow * a.ld_counts + v0);
-      const int4 p0 = p[0], p1 = p[1];
-      const int k[kVecTokens] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-#pragma unroll
-      for (int e = 0; e < kVecTokens; ++e) c[e] = (seen >> e) & 1 ? (float)k[e] : 0.0f;
-    }
-  }
-  const char* src = a.logits + (int64_t)row0 * a.ld_bytes + (int64_t)v0 * (Oct<BF16>::kBytes / kVecTokens);
-  char* dst = a.out + (src - a.logits);
-  const uint8_t* mask = m0 >= 0 ? (const uint8_t*)(a.mask + (int64_t)m0 * a.ld_mask) + (v0 >> 3) : nullptr;
-  const bool copy = a.out != a.logits;
-  for (int i = 0; i < n; ++i) {
-    if (i > 0 && pen && draft) {
-      const int x = draft[i - 1];
-#pragma unroll
-      for (int e = 0; e < kVecTokens; ++e)
-        if (x == v0 + e) {
-          c[e] += 1.0f;
-          seen |= 1u << e;
-        }
-    }
-    const unsigned allowed = mask ? mask[(int64_t)i * a.ld_mask * 4] : 0xFFu;
-    const unsigned touched = seen | biased | (allowed ^ 0xFFu);
-    if (copy || touched) {
-      float x[kVecTokens];
-      Oct<BF16>::load(src, x);
-#pragma unroll
-      for (int e = 0; e < kVecTokens; ++e) {
-        if ((seen >> e) & 1) {
-          x[e] = x[e] > 0.0f ? x[e] / rep : x[e] * rep;
-          x[e] -= freq * c[e];
-          if (c[e] > 0.0f) x[e] -= pres;
-        }
-        if ((biased >> e) & 1) x[e] += bias[e];
-        if (!((allowed >> e) & 1)) x[e] = -inf;
-      }
-      Oct<BF16>::store(dst, x);
-    }
-    src += a.ld_bytes;
-    dst += a.ld_bytes;
   }
 }
 
@@ -300,12 +386,21 @@ extern "C" int sd_logit_shape(hipStream_t stream, int R, int gamma_max, int V, i
   a.ld_mask = ld_mask;
   a.n_mask_rows = n_mask_rows;
   const long long items = (long long)R * a.n_ch;
-  if (items > 0xFFFFFFFFLL / kShapeThreads) return SD_EUNSUPPORTED;  // work-items of one launch
-  const dim3 g((unsigned)items), b(kShapeThreads);
+  const int rows = gamma_max + 1;
+  const long long spare = kFullWaves / (items > 0 ? items : 1);   // waves a request's rows may be split over
+  const int groups = spare < 1 ? 1 : (spare < rows ? (int)spare : rows);
+  a.group = (rows + groups - 1) / groups;
+  if (items * groups > 0xFFFFFFFFLL / kShapeThreads) return SD_EUNSUPPORTED;  // work-items of one launch
+  const dim3 g((unsigned)items, groups), b(kShapeThreads);
+  const bool nt = (double)R * rows * a.ld_bytes * (out != logits ? 2 : 1) > kCacheBytes;
+  hipError_t e;
   if (dtype == SD_DTYPE_BF16)
-    SDV_TRY_LAUNCH(sdv::launch(k_logit_shape<true>, g, b, 0, stream, a));
+    e = nt ? sdv::launch(k_logit_shape<true, true>, g, b, 0, stream, a)
+           : sdv::launch(k_logit_shape<true, false>, g, b, 0, stream, a);
   else
-    SDV_TRY_LAUNCH(sdv::launch(k_logit_shape<false>, g, b, 0, stream, a));
+    e = nt ? sdv::launch(k_logit_shape<false, true>, g, b, 0, stream, a)
+           : sdv::launch(k_logit_shape<false, false>, g, b, 0, stream, a);
+  SDV_TRY_LAUNCH(e);
   return SD_OK;
 }
 
