@@ -334,6 +334,13 @@ def test_counts_of_one_row_shared_by_requests():
     _counts_check([g.integers(0, 64, 500) for _ in range(6)], 64, slot=[2, 2, 0, 2, 0, 2], reset=[1, 0, 0, 1, 0, 0])
 
 
+def test_counts_of_very_many_requests():
+    g = np.random.default_rng(6)
+    R = 4100
+    _counts_check([g.integers(0, 40, k) for k in g.integers(0, 6, R)], 40, slot=g.permutation(R),
+                  reset=(g.random(R) < 0.5).astype(int), prompt=g.integers(0, 4, R))
+
+
 def test_counts_skip_tokens_outside_and_requests_out_of_range():
     V = 64
     i32 = lambda a: torch.as_tensor(a, dtype=torch.int32).to(DEV)  # noqa: E731
