@@ -434,51 +434,56 @@ def sd_lightspec_plan(ema, count, d_prev, sps, draft_cost, out=None, workspace=N
                 b_next=b_next, phi=phi)
 
 
+# The handle of a device's current stream, without a stream object in between.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on_device(fn):
-    """Run fn with the device of its first argument as torch's current one, so
-    that the kernels are launched, and outputs made, where the tensors live;
-    a given stream has to be that device's."""
+    """Run fn with the device of its first argument as torch's current one and
+    its `stream` argument, where given, as the current stream (see _on_stream),
+    so that the kernels are launched, and outputs made, where the tensors live.
+    The stream has to be that device's."""
     name = next(iter(inspect.signature(fn).parameters))
 
     @functools.wraps(fn)
     def wrapper(*args, **kw):
-        dev = getattr(args[0] if args else kw.get(name), "device", None)
-        if dev is None or dev.type != "cuda":
-            return fn(*args, **kw)   # which refuses it
+        first = args[0] if args else kw.get(name)
+        if not isinstance(first, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        index = first.get_device()
+        if index < 0:
+            raise ValueError(f"{name} must live on the GPU")
         stream = kw.get("stream")
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-        if dev.index == torch.cuda.current_device():
-            return fn(*args, **kw)
-        with torch.cuda.device(dev):
+        if stream is None:
+            if index == torch.cuda.current_device():
+                return fn(*args, **kw)
+            with torch.cuda.device(index):
+                return fn(*args, **kw)
+        if stream.device_index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
+        with torch.cuda.stream(stream):
             return fn(*args, **kw)
     return wrapper
 
 
-def _ptr_on(t, dtype, name, dev, shape=None):
-    """The address of tensor t (None: NULL) after checking its type, its
-    device, that it is contiguous, and its shape where given."""
+def _arg(t, dtype, name, index, n=None):
+    """The address of tensor t (None: NULL) after checking its type, that it
+    is contiguous and on device `index`, and its number of elements where
+    given."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype is dtype and t.get_device() == index and t.is_contiguous() and (n is None or t.numel() == n):
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} must live on {dev}, not {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must live on cuda:{index}, not {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    return t.data_ptr()
-
-
-def _device_of(t, name):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must live on the GPU")
-    return t.device
+    raise ValueError(f"{name} must hold {n} elements, got shape {list(t.shape)}")
 
 
 def _state_rows(seen, counts, V):
@@ -493,7 +498,6 @@ def _state_rows(seen, counts, V):
 
 
 @_on_device
-@_on_stream
 def sd_logit_shape(logits, row0, ell, V, gamma_max=None, draft_tokens=None, repetition=None, frequency=None,
                    presence=None, seen=None, counts=None, slot=None, bias=None, mask=None, mask_row0=None,
                    out=None, *, stream=None):
@@ -507,7 +511,7 @@ def sd_logit_shape(logits, row0, ell, V, gamma_max=None, draft_tokens=None, repe
     out["logits"] may be logits itself (in place); without it new rows are
     made, whose parts outside the batch are undefined.  Returns a dict of
     device tensors: logits, status."""
-    dev = _device_of(logits, "logits")
+    dev = logits.get_device()
     if logits.dim() != 2:
         raise ValueError("logits must be 2-D")
     n_rows, ld = logits.shape
@@ -526,33 +530,33 @@ def sd_logit_shape(logits, row0, ell, V, gamma_max=None, draft_tokens=None, repe
         raise TypeError("logits must be bf16 or fp32")
     n_slots, ld_seen, ld_counts = _state_rows(seen, counts, V)
     b_off, b_tok, b_val = (None, None, None) if bias is None else bias
+    n_bias = 0 if b_tok is None else b_tok.numel()
     if (mask is None) != (mask_row0 is None):
         raise ValueError("mask and mask_row0 go together")
     if mask is not None and mask.dim() != 2:
         raise ValueError("mask must be 2-D")
     o = out or {}
     dst = _out(o, "logits", lambda: torch.empty_like(logits))
-    status = _out(o, "status", lambda: torch.empty(R, dtype=torch.int32, device=dev))
-    i32, f32, n = torch.int32, torch.float32, (R,)
+    status = _out(o, "status", lambda: torch.empty(R, dtype=torch.int32, device=logits.device))
+    if dst.shape != logits.shape:
+        raise ValueError(f"out must have the logits' shape {list(logits.shape)}, got {list(dst.shape)}")
+    i32, f32, ldt = torch.int32, torch.float32, logits.dtype
     code = lib().sd_logit_shape(
-        _stream(stream), R, int(gamma_max), int(V), ld, dt, _ptr_on(logits, logits.dtype, "logits", dev),
-        _ptr_on(dst, logits.dtype, "out", dev, logits.shape), n_rows, _ptr_on(row0, i32, "row0", dev),
-        _ptr_on(ell, i32, "ell", dev, n),
-        None if draft_tokens is None else _ptr_on(draft_tokens, i32, "draft_tokens", dev, (R, gamma_max)),
-        _ptr_on(repetition, f32, "repetition", dev, n), _ptr_on(frequency, f32, "frequency", dev, n),
-        _ptr_on(presence, f32, "presence", dev, n), _ptr_on(seen, i32, "seen", dev), ld_seen,
-        _ptr_on(counts, i32, "counts", dev), ld_counts, n_slots, _ptr_on(slot, i32, "slot", dev, n),
-        _ptr_on(b_off, torch.int64, "bias offsets", dev, (R + 1,)), _ptr_on(b_tok, i32, "bias tokens", dev),
-        None if bias is None else _ptr_on(b_val, f32, "bias values", dev, b_tok.shape),
-        0 if bias is None else b_tok.numel(), _ptr_on(mask, i32, "mask", dev),
-        0 if mask is None else mask.shape[1], 0 if mask is None else mask.shape[0],
-        _ptr_on(mask_row0, i32, "mask_row0", dev, n), _ptr_on(status, i32, "status", dev, n))
+        _raw_stream(dev), R, int(gamma_max), int(V), ld, dt, _arg(logits, ldt, "logits", dev),
+        _arg(dst, ldt, "out", dev), n_rows, _arg(row0, i32, "row0", dev), _arg(ell, i32, "ell", dev, R),
+        _arg(draft_tokens, i32, "draft_tokens", dev, R * gamma_max), _arg(repetition, f32, "repetition", dev, R),
+        _arg(frequency, f32, "frequency", dev, R), _arg(presence, f32, "presence", dev, R),
+        _arg(seen, i32, "seen", dev), ld_seen, _arg(counts, i32, "counts", dev), ld_counts, n_slots,
+        _arg(slot, i32, "slot", dev, R), _arg(b_off, torch.int64, "bias offsets", dev, R + 1),
+        _arg(b_tok, i32, "bias tokens", dev), _arg(b_val, f32, "bias values", dev, n_bias), n_bias,
+        _arg(mask, i32, "mask", dev), 0 if mask is None else mask.shape[1],
+        0 if mask is None else mask.shape[0], _arg(mask_row0, i32, "mask_row0", dev, R),
+        _arg(status, i32, "status", dev, R))
     _check("sd_logit_shape", code)
     return dict(logits=dst, status=status)
 
 
 @_on_device
-@_on_stream
 def sd_token_counts(tokens, seen, counts, V, start=None, length=None, prompt_len=None, slot=None, reset=None,
                     out=None, *, stream=None):
     """Enter token lists into the state behind the penalties, in place: seen
@@ -562,7 +566,7 @@ def sd_token_counts(tokens, seen, counts, V, start=None, length=None, prompt_len
     start [R] int64 and length.  prompt_len [R] int32: how many leading tokens
     of each list are prompt; reset [R] int32: clear the state row first.
     Returns a dict: status."""
-    dev = _device_of(tokens, "tokens")
+    dev = tokens.get_device()
     if start is not None:
         R, width = start.numel(), 0
         if length is None:
@@ -574,14 +578,14 @@ def sd_token_counts(tokens, seen, counts, V, start=None, length=None, prompt_len
     if seen is None:
         raise ValueError("seen is needed")
     n_slots, ld_seen, ld_counts = _state_rows(seen, counts, V)
-    status = _out(out or {}, "status", lambda: torch.empty(R, dtype=torch.int32, device=dev))
-    i32, n = torch.int32, (R,)
+    status = _out(out or {}, "status", lambda: torch.empty(R, dtype=torch.int32, device=tokens.device))
+    i32 = torch.int32
     code = lib().sd_token_counts(
-        _stream(stream), R, int(V), _ptr_on(tokens, i32, "tokens", dev), tokens.numel(), width,
-        _ptr_on(start, torch.int64, "start", dev), _ptr_on(length, i32, "length", dev, n),
-        _ptr_on(prompt_len, i32, "prompt_len", dev, n), _ptr_on(slot, i32, "slot", dev, n),
-        _ptr_on(reset, i32, "reset", dev, n), _ptr_on(seen, i32, "seen", dev), ld_seen,
-        _ptr_on(counts, i32, "counts", dev), ld_counts, n_slots, _ptr_on(status, i32, "status", dev, n))
+        _raw_stream(dev), R, int(V), _arg(tokens, i32, "tokens", dev), tokens.numel(), width,
+        _arg(start, torch.int64, "start", dev), _arg(length, i32, "length", dev, R),
+        _arg(prompt_len, i32, "prompt_len", dev, R), _arg(slot, i32, "slot", dev, R),
+        _arg(reset, i32, "reset", dev, R), _arg(seen, i32, "seen", dev), ld_seen,
+        _arg(counts, i32, "counts", dev), ld_counts, n_slots, _arg(status, i32, "status", dev, R))
     _check("sd_token_counts", code)
     return dict(status=status)
 
@@ -591,7 +595,6 @@ def sd_slot_reserve_workspace_size(R):
 
 
 @_on_device
-@_on_stream
 def sd_slot_reserve(seq_len, ell, block_table, free_list, free_count, block_size, q_max, max_rows=None,
                     padded=False, x0=None, tokens=None, out=None, workspace=None, *, stream=None):
     """Rows and cache slots of a step.  seq_len [R] int64, ell [R] int32
@@ -602,7 +605,7 @@ def sd_slot_reserve(seq_len, ell, block_table, free_list, free_count, block_size
     out["row_req"]).  Returns a dict of device tensors: ell, row0, cu_rows,
     ctx_len, batch, free_count, row_req, row_pos, row_slot, row_token (None
     without tokens), status."""
-    dev = _device_of(seq_len, "seq_len")
+    dev, device = seq_len.get_device(), seq_len.device
     R = seq_len.numel()
     if block_table.dim() != 2 or (tokens is not None and tokens.dim() != 2):
         raise ValueError("block_table and tokens must be 2-D")
@@ -611,29 +614,28 @@ def sd_slot_reserve(seq_len, ell, block_table, free_list, free_count, block_size
     i32 = torch.int32
     if max_rows is None:
         max_rows = o["row_req"].numel() if "row_req" in o else R * q_max
-    make = lambda k, dt=i32: (lambda: torch.empty(k, dtype=dt, device=dev))  # noqa: E731
-    res = dict(ell=_out(o, "ell", make(R)), row0=_out(o, "row0", make(R)), cu_rows=_out(o, "cu_rows", make(R + 1)),
-               ctx_len=_out(o, "ctx_len", make(R)), batch=_out(o, "batch", make(1)),
-               free_count=_out(o, "free_count", make(1)), row_req=_out(o, "row_req", make(max_rows)),
-               row_pos=_out(o, "row_pos", make(max_rows)),
-               row_slot=_out(o, "row_slot", make(max_rows, torch.int64)),
-               row_token=None if x0 is None and tokens is None else _out(o, "row_token", make(max_rows)),
-               status=_out(o, "status", make(R)))
-    ws = workspace if workspace is not None else _workspace(sd_slot_reserve_workspace_size(R), dev)
-    n, m, one = (R,), (max_rows,), (1,)
+    i64 = torch.int64
+    make = lambda k, dt=i32: torch.empty(k, dtype=dt, device=device)  # noqa: E731
+    with_tokens = x0 is not None or tokens is not None
+    res = {k: o[k] if k in o else make(size)
+           for k, size in (("ell", R), ("row0", R), ("cu_rows", R + 1), ("ctx_len", R), ("batch", 1),
+                           ("free_count", 1), ("row_req", max_rows), ("row_pos", max_rows), ("status", R))}
+    res["row_slot"] = o["row_slot"] if "row_slot" in o else make(max_rows, i64)
+    res["row_token"] = None if not with_tokens else o["row_token"] if "row_token" in o else make(max_rows)
+    ws = workspace if workspace is not None else _workspace(sd_slot_reserve_workspace_size(R), device)
     code = lib().sd_slot_reserve(
-        _stream(stream), R, int(q_max), int(block_size), mb, free_list.numel(), max_rows, 1 if padded else 0,
-        _ptr_on(seq_len, torch.int64, "seq_len", dev), _ptr_on(ell, i32, "ell", dev, n),
-        _ptr_on(x0, i32, "x0", dev, n), _ptr_on(tokens, i32, "tokens", dev),
-        0 if tokens is None else tokens.shape[1], _ptr_on(block_table, i32, "block_table", dev, (R, mb)),
-        _ptr_on(free_list, i32, "free_list", dev), _ptr_on(free_count, i32, "free_count", dev, one),
-        _ptr_on(res["ell"], i32, "out ell", dev, n), _ptr_on(res["row0"], i32, "row0", dev, n),
-        _ptr_on(res["cu_rows"], i32, "cu_rows", dev, (R + 1,)), _ptr_on(res["ctx_len"], i32, "ctx_len", dev, n),
-        _ptr_on(res["batch"], i32, "batch", dev, one), _ptr_on(res["free_count"], i32, "out free_count", dev, one),
-        _ptr_on(res["row_req"], i32, "row_req", dev, m), _ptr_on(res["row_pos"], i32, "row_pos", dev, m),
-        _ptr_on(res["row_slot"], torch.int64, "row_slot", dev, m),
-        _ptr_on(res["row_token"], i32, "row_token", dev, m), _ptr_on(res["status"], i32, "status", dev, n),
-        _ptr_on(ws, torch.uint8, "workspace", dev), ws.numel())
+        _raw_stream(dev), R, int(q_max), int(block_size), mb, free_list.numel(), max_rows, 1 if padded else 0,
+        _arg(seq_len, i64, "seq_len", dev), _arg(ell, i32, "ell", dev, R), _arg(x0, i32, "x0", dev, R),
+        _arg(tokens, i32, "tokens", dev, None if tokens is None else R * tokens.shape[1]),
+        0 if tokens is None else tokens.shape[1], _arg(block_table, i32, "block_table", dev, R * mb),
+        _arg(free_list, i32, "free_list", dev), _arg(free_count, i32, "free_count", dev, 1),
+        _arg(res["ell"], i32, "out ell", dev, R), _arg(res["row0"], i32, "row0", dev, R),
+        _arg(res["cu_rows"], i32, "cu_rows", dev, R + 1), _arg(res["ctx_len"], i32, "ctx_len", dev, R),
+        _arg(res["batch"], i32, "batch", dev, 1), _arg(res["free_count"], i32, "out free_count", dev, 1),
+        _arg(res["row_req"], i32, "row_req", dev, max_rows), _arg(res["row_pos"], i32, "row_pos", dev, max_rows),
+        _arg(res["row_slot"], i64, "row_slot", dev, max_rows),
+        _arg(res["row_token"], i32, "row_token", dev, max_rows), _arg(res["status"], i32, "status", dev, R),
+        _arg(ws, torch.uint8, "workspace", dev), ws.numel())
     _check("sd_slot_reserve", code)
     return res
 
@@ -643,7 +645,6 @@ def sd_slot_commit_workspace_size(R):
 
 
 @_on_device
-@_on_stream
 def sd_slot_commit(seq_len, ell, n_acc, block_table, free_list, free_count, block_size, q_max=None,
                    out_tokens=None, x0=None, status=None, release=None, keep=None, out=None, workspace=None,
                    *, stream=None):
@@ -654,7 +655,7 @@ def sd_slot_commit(seq_len, ell, n_acc, block_table, free_list, free_count, bloc
     returned); release, keep [R] int32.  free_list is updated in place, and
     status where a request is refused.  Returns a dict of device tensors:
     seq_len, n_new, free_count, x0 (None without out_tokens)."""
-    dev = _device_of(seq_len, "seq_len")
+    dev, device = seq_len.get_device(), seq_len.device
     R = seq_len.numel()
     if block_table.dim() != 2:
         raise ValueError("block_table must be 2-D")
@@ -667,23 +668,22 @@ def sd_slot_commit(seq_len, ell, n_acc, block_table, free_list, free_count, bloc
         raise ValueError("q_max is needed without out_tokens")
     o = out or {}
     i32 = torch.int32
-    res = dict(seq_len=_out(o, "seq_len", lambda: torch.empty(R, dtype=torch.int64, device=dev)),
-               n_new=_out(o, "n_new", lambda: torch.empty(R, dtype=i32, device=dev)),
-               free_count=_out(o, "free_count", lambda: torch.empty(1, dtype=i32, device=dev)),
-               x0=None if out_tokens is None
-               else _out(o, "x0", lambda: torch.empty(R, dtype=i32, device=dev)))
-    ws = workspace if workspace is not None else _workspace(sd_slot_commit_workspace_size(R), dev)
-    n, one = (R,), (1,)
+    i64 = torch.int64
+    make = lambda k, dt=i32: torch.empty(k, dtype=dt, device=device)  # noqa: E731
+    res = dict(seq_len=o["seq_len"] if "seq_len" in o else make(R, i64),
+               n_new=o["n_new"] if "n_new" in o else make(R),
+               free_count=o["free_count"] if "free_count" in o else make(1),
+               x0=None if out_tokens is None else o["x0"] if "x0" in o else make(R))
+    ws = workspace if workspace is not None else _workspace(sd_slot_commit_workspace_size(R), device)
     code = lib().sd_slot_commit(
-        _stream(stream), R, int(q_max), int(block_size), mb, free_list.numel(),
-        _ptr_on(seq_len, torch.int64, "seq_len", dev), _ptr_on(ell, i32, "ell", dev, n),
-        _ptr_on(n_acc, i32, "n_acc", dev, n),
-        None if out_tokens is None else _ptr_on(out_tokens, i32, "out_tokens", dev, (R, q_max)),
-        _ptr_on(x0, i32, "x0", dev, n), _ptr_on(release, i32, "release", dev, n), _ptr_on(keep, i32, "keep", dev, n),
-        _ptr_on(block_table, i32, "block_table", dev, (R, mb)), _ptr_on(free_list, i32, "free_list", dev),
-        _ptr_on(free_count, i32, "free_count", dev, one), _ptr_on(status, i32, "status", dev, n),
-        _ptr_on(res["seq_len"], torch.int64, "out seq_len", dev, n), _ptr_on(res["x0"], i32, "out x0", dev, n),
-        _ptr_on(res["n_new"], i32, "n_new", dev, n), _ptr_on(res["free_count"], i32, "out free_count", dev, one),
-        _ptr_on(ws, torch.uint8, "workspace", dev), ws.numel())
+        _raw_stream(dev), R, int(q_max), int(block_size), mb, free_list.numel(),
+        _arg(seq_len, i64, "seq_len", dev), _arg(ell, i32, "ell", dev, R), _arg(n_acc, i32, "n_acc", dev, R),
+        _arg(out_tokens, i32, "out_tokens", dev, R * q_max), _arg(x0, i32, "x0", dev, R),
+        _arg(release, i32, "release", dev, R), _arg(keep, i32, "keep", dev, R),
+        _arg(block_table, i32, "block_table", dev, R * mb), _arg(free_list, i32, "free_list", dev),
+        _arg(free_count, i32, "free_count", dev, 1), _arg(status, i32, "status", dev, R),
+        _arg(res["seq_len"], i64, "out seq_len", dev, R), _arg(res["x0"], i32, "out x0", dev, R),
+        _arg(res["n_new"], i32, "n_new", dev, R), _arg(res["free_count"], i32, "out free_count", dev, 1),
+        _arg(ws, torch.uint8, "workspace", dev), ws.numel())
     _check("sd_slot_commit", code)
     return res

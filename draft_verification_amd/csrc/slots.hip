@@ -14,31 +14,46 @@ namespace {
 constexpr int kScanThreads = 1024;
 constexpr int kScanWaves = kScanThreads / 64;
 constexpr int kFillThreads = 256;
+constexpr int kOneLaunchRequests = 1024;  // requests whose scan a workgroup keeps in LDS
+constexpr int kOneLaunchGrid = 1024;      // workgroups that repeat the scan
+constexpr int kCommitRequests = 4;        // requests per workgroup of k_commit_all
 
-// Exclusive prefix sum over the workgroup; *total gets the sum.
-SDV_DEV int block_scan(int v, int* part, int* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int s = v;
+// As many waves as the requests fill, up to a workgroup.
+unsigned scan_threads(int R) { return R >= kScanThreads ? kScanThreads : (unsigned)(R + 63) / 64 * 64; }
+
+// Exclusive prefix sums over the workgroup of two counts below 2^31, one in
+// each half of a word (their sums stay below 2^31: the halves do not mix);
+// *total gets the sums.
+SDV_DEV uint64_t block_scan(uint64_t v, uint64_t* part, uint64_t* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  uint64_t s = v;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const int t = __shfl_up(s, o, 64);
+    const uint64_t t = __shfl_up((unsigned long long)s, o, 64);
     if (lane >= o) s += t;
+  }
+  if (waves == 1) {
+    *total = __shfl((unsigned long long)s, 63, 64);
+    return s - v;
   }
   __syncthreads();   // part may still be read from the last call
   if (lane == 63) part[wave] = s;
   __syncthreads();
-  int before = 0, sum = 0;
-#pragma unroll
-  for (int w = 0; w < kScanWaves; ++w) {
-    const int p = part[w];
+  uint64_t before = 0, sum = 0;
+  for (int w = 0; w < waves; ++w) {
+    const uint64_t p = part[w];
     if (w < wave) before += p;
     sum += p;
   }
   *total = sum;
   return before + s - v;
 }
+SDV_DEV uint64_t two(int hi, int lo) { return (uint64_t)(uint32_t)hi << 32 | (uint32_t)lo; }
+SDV_DEV int hi_of(uint64_t v) { return (int)(v >> 32); }
+SDV_DEV int lo_of(uint64_t v) { return (int)(uint32_t)v; }
 
-SDV_DEV int blocks_of(int64_t n, int bs) { return (int)((n + bs - 1) / bs); }
+// Blocks that hold n positions; n and bs below 2^31 - 256 as all positions are.
+SDV_DEV int blocks_of(int n, int bs) { return (int)(((unsigned)n + (unsigned)bs - 1u) / (unsigned)bs); }
 
 struct ReserveArgs {
   const int64_t* seq_len;
@@ -65,67 +80,235 @@ struct ReserveArgs {
   int R, q_max, bs, max_blocks, n_blocks, max_rows, padded, ld_tokens;
 };
 
-__global__ __launch_bounds__(kScanThreads) void k_reserve_scan(ReserveArgs a) {
-  __shared__ int part[kScanWaves];
+SDV_DEV void no_row(const ReserveArgs& a, int e) {
+  a.row_req[e] = -1;
+  a.row_pos[e] = -1;
+  a.row_slot[e] = -1;
+  if (a.row_token) a.row_token[e] = -1;
+}
+
+struct Reserved {
+  int len;     // tokens in the cache
+  int n;       // rows
+  int row;     // rows of the requests before
+  int first;   // index in the free list of the first new block, counting down
+  int st;
+};
+
+// What each request gets, kItems requests per thread, whose loads are
+// requested together.  Three quantities depend on the requests before: the
+// rows that fit the buffers, the blocks that are left, and where the rows
+// begin.  Each is a prefix sum; the last two are one while the blocks suffice.
+// emit(r, Reserved) is called by one thread per request; every thread gets
+// the totals.
+template <int kItems, typename Emit>
+SDV_DEV void reserve_scan(const ReserveArgs& a, uint64_t* part, int* rows, int* free_left, Emit emit) {
   const int64_t cap = (int64_t)a.bs * a.max_blocks;
   const int F = sdv::clampi(*a.free_count, 0, a.n_blocks);
-  int want_before = 0, need_before = 0, rows_before = 0, taken = 0;
-  for (int t = 0; t < a.R; t += kScanThreads) {
-    const int r = t + threadIdx.x;
-    int64_t len = 0;
-    int asked = 0, st = 0;
-    if (r < a.R) {
-      len = a.seq_len[r];
-      asked = min(a.ell[r], a.q_max - 1) + 1;
-      if (asked < 0) asked = 0;
-      if (len < 0 || len > cap) {
-        st = SD_ST_BAD_INPUT;
-        len = 0;
-        asked = 0;
+  const bool may_cut = !a.padded && a.max_rows < a.R * a.q_max;   // rows may not fit the buffers
+  int want_before = 0, need_before = 0, rows_before = 0;
+  for (int t = 0; t < a.R; t += blockDim.x * kItems) {
+    const int r0 = t + threadIdx.x * kItems;
+    int64_t len[kItems];
+    int asked[kItems], want[kItems], h0[kItems], need[kItems], n[kItems], st[kItems];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      len[k] = r0 + k < a.R ? a.seq_len[r0 + k] : 0;
+      asked[k] = r0 + k < a.R ? a.ell[r0 + k] : -1;
+    }
+    int wants = 0, needs = 0;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      asked[k] = max(min(asked[k], a.q_max - 1) + 1, 0);
+      st[k] = 0;
+      if (len[k] < 0 || len[k] > cap) {
+        st[k] = SD_ST_BAD_INPUT;
+        len[k] = 0;
+        asked[k] = 0;
+      }
+      want[k] = (int)(asked[k] < cap - len[k] ? asked[k] : cap - len[k]);
+      wants += want[k];
+    }
+    uint64_t total;
+    if (may_cut) {
+      int before = lo_of(block_scan(two(0, wants), part, &total)) + want_before;
+      want_before += lo_of(total);
+      wants = 0;
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        const int wished = want[k];
+        want[k] = sdv::clampi(a.max_rows - before, 0, wished);
+        before += wished;
+        wants += want[k];
       }
     }
-    int want = (int)(asked < cap - len ? asked : cap - len);
-    int total;
-    int before = block_scan(want, part, &total) + want_before;
-    want_before += total;
-    if (!a.padded) want = sdv::clampi(a.max_rows - before, 0, want);
-    const int h0 = blocks_of(len, a.bs);
-    const int need = blocks_of(len + want, a.bs) - h0;
-    before = block_scan(need, part, &total) + need_before;
-    need_before += total;
-    const int got = sdv::clampi(F - before, 0, need);
-    const int64_t room = (int64_t)(h0 + got) * a.bs - len;
-    const int n = (int)(want < room ? want : room);
-    const int first = F - 1 - before;
-    before = block_scan(n, part, &total) + rows_before;
-    rows_before += total;
-    block_scan(got, part, &total);
-    taken += total;
-    if (r < a.R) {
-      if (n < asked) st |= SD_ST_NO_SLOT;
-      const bool bad = (st & SD_ST_BAD_INPUT) != 0;
-      a.ws_first[r] = first;
-      a.ws_base[r] = (int32_t)len;
-      a.ws_cu[r] = before;
-      a.ell_out[r] = n - 1;
-      a.row0[r] = a.padded ? r * a.q_max : min(before, a.max_rows - 1);
-      a.cu_rows[r] = before;
-      a.ctx_len[r] = bad ? 0 : (int32_t)(len + n);
-      a.status[r] = st;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      h0[k] = blocks_of((int)len[k], a.bs);
+      need[k] = blocks_of((int)len[k] + want[k], a.bs) - h0[k];
+      n[k] = want[k];
+      needs += need[k];
+    }
+    const uint64_t pre = block_scan(two(needs, wants), part, &total);
+    int spoken = hi_of(pre) + need_before, before = lo_of(pre);
+    need_before += hi_of(total);
+    if (need_before > F) {   // the blocks run out in this tile or did before
+      int sum = 0, taken = spoken;
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        const int got = sdv::clampi(F - taken, 0, need[k]);
+        const int64_t room = (int64_t)(h0[k] + got) * a.bs - len[k];
+        n[k] = (int)(want[k] < room ? want[k] : room);
+        taken += need[k];
+        sum += n[k];
+      }
+      before = lo_of(block_scan(two(0, sum), part, &total));
+    }
+    before += rows_before;
+    rows_before += lo_of(total);
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      if (n[k] < asked[k]) st[k] |= SD_ST_NO_SLOT;
+      if (r0 + k < a.R) emit(r0 + k, Reserved{(int)len[k], n[k], before, F - 1 - spoken, st[k]});
+      before += n[k];
+      spoken += need[k];
     }
   }
-  if (threadIdx.x == 0) {
-    a.ws_cu[a.R] = rows_before;
-    a.cu_rows[a.R] = rows_before;
-    *a.batch = rows_before;
-    *a.free_out = F - taken;
+  *rows = rows_before;
+  *free_left = F - min(F, need_before);
+}
+
+SDV_DEV void reserve_out(const ReserveArgs& a, int r, const Reserved& q) {
+  a.ell_out[r] = q.n - 1;
+  a.row0[r] = a.padded ? r * a.q_max : min(q.row, a.max_rows - 1);
+  a.cu_rows[r] = q.row;
+  a.ctx_len[r] = (q.st & SD_ST_BAD_INPUT) ? 0 : q.len + q.n;
+}
+
+// One row of a request: its position's slot and its token.
+SDV_DEV void fill_row(const ReserveArgs& a, int e, int r, int i, int len, int first) {
+  const int pos = len + i, b = (int)((unsigned)pos / (unsigned)a.bs), off = pos - b * a.bs;
+  const int h0 = blocks_of(len, a.bs);
+  const int block = b < h0 ? a.table[(int64_t)r * a.max_blocks + b] : a.free_list[first - (b - h0)];
+  a.row_req[e] = r;
+  a.row_pos[e] = pos;
+  a.row_slot[e] = block >= 0 && block < a.n_blocks ? (int64_t)block * a.bs + off : -1;
+  if (a.row_token) {
+    const int32_t* t = a.tokens + (int64_t)r * a.ld_tokens;
+    a.row_token[e] = a.x0 ? (i == 0 ? a.x0[r] : t[i - 1]) : t[i];
   }
 }
 
-// One thread per row of the buffers: its request, position, slot and token;
-// the first row of a new block also enters the block into the table.
+// The new blocks of a request into its table, by one wave; true where one of
+// the blocks of its rows is outside the pool.
+SDV_DEV bool enter_blocks(const ReserveArgs& a, int r, int len, int n, int first) {
+  const int lane = threadIdx.x & 63, h0 = blocks_of(len, a.bs);
+  const int got = blocks_of(len + n, a.bs) - h0;
+  int32_t* table = a.table + (int64_t)r * a.max_blocks + h0;
+  bool bad = false;
+  if (lane == 0 && n > 0 && len % a.bs != 0) {   // rows begin inside a block
+    const int b = table[-1];
+    bad = b < 0 || b >= a.n_blocks;
+  }
+  for (int k = lane; k < got; k += 64) {
+    const int b = a.free_list[first - k];
+    bad |= b < 0 || b >= a.n_blocks;
+    table[k] = b;
+  }
+  return __ballot(bad) != 0;
+}
+
+// One launch: every workgroup repeats the scan (a few thousand words from
+// cache, no second launch to wait for), then its waves take requests and its
+// threads rows.  No output may be an input here unless the grid is one
+// workgroup.
+template <int kItems>
+__global__ __launch_bounds__(kFillThreads) void k_reserve_all(ReserveArgs a) {
+  __shared__ uint64_t part[kScanWaves];
+  __shared__ int cu[kOneLaunchRequests + 1], len[kOneLaunchRequests], first[kOneLaunchRequests];
+  __shared__ uint8_t st[kOneLaunchRequests];
+  int rows, left;
+  reserve_scan<kItems>(a, part, &rows, &left, [&](int r, const Reserved& q) {
+    cu[r] = q.row;
+    len[r] = q.len;
+    first[r] = q.first;
+    st[r] = (uint8_t)q.st;
+  });
+  if (threadIdx.x == 0) cu[a.R] = rows;
+  __syncthreads();   // and free_count has been read by all
+  const int waves = gridDim.x * (kFillThreads / 64);
+  for (int r = blockIdx.x * (kFillThreads / 64) + (threadIdx.x >> 6); r < a.R; r += waves) {
+    const Reserved q{len[r], cu[r + 1] - cu[r], cu[r], first[r], st[r]};
+    const bool bad = enter_blocks(a, r, q.len, q.n, q.first);
+    if ((threadIdx.x & 63) == 0) {
+      reserve_out(a, r, q);
+      a.status[r] = q.st | (bad ? SD_ST_BAD_INPUT : 0);
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.cu_rows[a.R] = rows;
+    *a.batch = rows;
+    *a.free_out = left;
+  }
+  for (int64_t e64 = (int64_t)blockIdx.x * kFillThreads + threadIdx.x; e64 < a.max_rows;
+       e64 += (int64_t)gridDim.x * kFillThreads) {
+    const int e = (int)e64;
+    int lo = 0, i;
+    if (a.padded) {
+      lo = e / a.q_max;
+      i = e - lo * a.q_max;
+      if (lo >= a.R || i >= cu[lo + 1] - cu[lo]) {
+        no_row(a, e);
+        continue;
+      }
+    } else {
+      if (e >= rows) {
+        no_row(a, e);
+        continue;
+      }
+      int hi = a.R;   // cu[lo] <= e < cu[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= e) lo = mid;
+        else hi = mid;
+      }
+      i = e - cu[lo];
+    }
+    fill_row(a, e, lo, i, len[lo], first[lo]);
+  }
+}
+
+// Two launches, for more requests or outputs in the place of inputs: the scan,
+// then the rows.
+template <int kItems>
+__global__ __launch_bounds__(kScanThreads) void k_reserve_scan(ReserveArgs a) {
+  __shared__ uint64_t part[kScanWaves];
+  int rows, left;
+  reserve_scan<kItems>(a, part, &rows, &left, [&](int r, const Reserved& q) {
+    a.ws_first[r] = q.first;
+    a.ws_base[r] = q.len;
+    a.ws_cu[r] = q.row;
+    reserve_out(a, r, q);
+    a.status[r] = q.st;
+  });
+  __syncthreads();   // free_out may be free_count, which every thread has read now
+  if (threadIdx.x == 0) {
+    a.ws_cu[a.R] = rows;
+    a.cu_rows[a.R] = rows;
+    *a.batch = rows;
+    *a.free_out = left;
+  }
+}
+
+// One wave per request for its blocks, and one thread per row.
 __global__ __launch_bounds__(kFillThreads) void k_reserve_rows(ReserveArgs a) {
   const int e = blockIdx.x * kFillThreads + threadIdx.x;
+  const int w = e >> 6, waves = gridDim.x * (kFillThreads / 64);
+  for (int r = w; r < a.R; r += waves) {
+    const int row = a.ws_cu[r];
+    if (enter_blocks(a, r, a.ws_base[r], a.ws_cu[r + 1] - row, a.ws_first[r]) && (e & 63) == 0)
+      a.status[r] |= SD_ST_BAD_INPUT;
+  }
   if (e >= a.max_rows) return;
   int r, i = 0;
   bool live;
@@ -135,7 +318,7 @@ __global__ __launch_bounds__(kFillThreads) void k_reserve_rows(ReserveArgs a) {
     live = r < a.R && i < a.ws_cu[r + 1] - a.ws_cu[r];
   } else {   // the request whose rows hold e: ws_cu[r] <= e < ws_cu[r + 1]
     live = e < a.ws_cu[a.R];
-    int lo = 0, hi = a.R;   // ws_cu[lo] <= e < ws_cu[hi]
+    int lo = 0, hi = a.R;
     while (live && hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (a.ws_cu[mid] <= e) lo = mid;
@@ -144,32 +327,8 @@ __global__ __launch_bounds__(kFillThreads) void k_reserve_rows(ReserveArgs a) {
     r = lo;
     if (live) i = e - a.ws_cu[r];
   }
-  if (!live) {
-    a.row_req[e] = -1;
-    a.row_pos[e] = -1;
-    a.row_slot[e] = -1;
-    if (a.row_token) a.row_token[e] = -1;
-    return;
-  }
-  const int len = a.ws_base[r], pos = len + i;
-  const int b = pos / a.bs, off = pos - b * a.bs;
-  const int h0 = (len + a.bs - 1) / a.bs;
-  int block;
-  if (b < h0) {
-    block = a.table[(int64_t)r * a.max_blocks + b];
-  } else {
-    block = a.free_list[a.ws_first[r] - (b - h0)];
-    if (off == 0) a.table[(int64_t)r * a.max_blocks + b] = block;
-  }
-  const bool good = block >= 0 && block < a.n_blocks;
-  if (!good) atomicOr(&a.status[r], SD_ST_BAD_INPUT);
-  a.row_req[e] = r;
-  a.row_pos[e] = pos;
-  a.row_slot[e] = good ? (int64_t)block * a.bs + off : -1;
-  if (a.row_token) {
-    const int32_t* t = a.tokens + (int64_t)r * a.ld_tokens;
-    a.row_token[e] = a.x0 ? (i == 0 ? a.x0[r] : t[i - 1]) : t[i];
-  }
+  if (live) fill_row(a, e, r, i, a.ws_base[r], a.ws_first[r]);
+  else no_row(a, e);
 }
 
 struct CommitArgs {
@@ -192,54 +351,122 @@ struct CommitArgs {
   int R, q_max, bs, max_blocks, n_blocks;
 };
 
-__global__ __launch_bounds__(kScanThreads) void k_commit_scan(CommitArgs a) {
-  __shared__ int part[kScanWaves];
+struct Committed {
+  int64_t len;   // tokens that stay
+  int n_new;
+  int acc;
+  int kept;      // blocks that stay
+  int give;      // blocks that go back ...
+  int to;        // ... and where in the free list
+  bool bad;
+};
+
+// What becomes of each request, kItems per thread; emit(r, Committed) by one thread per request,
+// every thread gets the new count.
+template <int kItems, typename Emit>
+SDV_DEV void commit_scan(const CommitArgs& a, uint64_t* part, int* free_out, Emit emit) {
   const int64_t cap = (int64_t)a.bs * a.max_blocks;
   const int F = sdv::clampi(*a.free_count, 0, a.n_blocks);
   int before_all = 0;
-  for (int t = 0; t < a.R; t += kScanThreads) {
-    const int r = t + threadIdx.x;
-    int kept = 0, give = 0;
-    if (r < a.R) {
-      const int64_t len = a.seq_len[r];
-      const int L = a.ell[r], st = a.status ? a.status[r] : 0;
-      const int q = L < 0 ? 0 : L + 1;
-      int64_t len1 = len;
-      int adv = 0, acc = 0;
-      if (len < 0 || len > cap || L >= a.q_max || len + q > cap) {
-        if (a.status) a.status[r] = st | SD_ST_BAD_INPUT;
-      } else {
-        acc = sdv::clampi(a.n_acc[r], 0, q ? L : 0);
-        adv = q && !(st & (SD_ST_NONFINITE | SD_ST_ZERO_Z)) ? acc + 1 : 0;
-        const bool done = a.release && a.release[r];
-        const int held = blocks_of(len + q, a.bs);
-        len1 = done ? 0 : len + adv;
-        kept = done ? sdv::clampi(a.keep ? a.keep[r] : 0, 0, held) : blocks_of(len1, a.bs);
-        give = held - kept;
-      }
-      a.seq_out[r] = len1;
-      a.n_new[r] = adv;
-      if (a.x0_out) a.x0_out[r] = adv ? a.out_tokens[(int64_t)r * a.q_max + acc] : a.x0[r];
+  for (int t = 0; t < a.R; t += blockDim.x * kItems) {
+    const int r0 = t + threadIdx.x * kItems;
+    Committed c[kItems];
+    int64_t len[kItems];
+    int L[kItems], st[kItems], acc[kItems], done[kItems], keep[kItems];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {   // all requested together
+      const bool in = r0 + k < a.R;
+      len[k] = in ? a.seq_len[r0 + k] : 0;
+      L[k] = in ? a.ell[r0 + k] : -1;
+      acc[k] = in ? a.n_acc[r0 + k] : 0;
+      st[k] = in && a.status ? a.status[r0 + k] : 0;
+      done[k] = in && a.release ? a.release[r0 + k] : 0;
+      keep[k] = in && a.keep ? a.keep[r0 + k] : 0;
     }
-    int total;
-    const int before = block_scan(give, part, &total) + before_all;
-    before_all += total;
-    if (r < a.R) {
+    int gives = 0;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const int q = L[k] < 0 ? 0 : L[k] + 1;
+      c[k] = Committed{len[k], 0, 0, 0, 0, 0, false};
+      if (len[k] < 0 || len[k] > cap || L[k] >= a.q_max || len[k] + q > cap) {
+        c[k].bad = true;
+      } else {
+        c[k].acc = sdv::clampi(acc[k], 0, q ? L[k] : 0);
+        c[k].n_new = q && !(st[k] & (SD_ST_NONFINITE | SD_ST_ZERO_Z)) ? c[k].acc + 1 : 0;
+        const int held = blocks_of((int)len[k] + q, a.bs);
+        c[k].len = done[k] ? 0 : len[k] + c[k].n_new;
+        c[k].kept = done[k] ? sdv::clampi(keep[k], 0, held) : blocks_of((int)c[k].len, a.bs);
+        c[k].give = held - c[k].kept;
+      }
+      gives += c[k].give;
+    }
+    uint64_t total;
+    int to = F + lo_of(block_scan(two(0, gives), part, &total)) + before_all;
+    before_all += lo_of(total);
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      c[k].to = to;
+      to += c[k].give;
       // more blocks than the pool has: the accounting was broken before
-      if (give && (int64_t)F + before + give > a.n_blocks && a.status) a.status[r] |= SD_ST_BAD_INPUT;
-      a.ws[3 * r] = kept;
-      a.ws[3 * r + 1] = give;
-      a.ws[3 * r + 2] = F + before;
+      if (c[k].give && to > a.n_blocks) c[k].bad = true;
+      if (r0 + k < a.R) emit(r0 + k, c[k]);
     }
   }
-  if (threadIdx.x == 0) *a.free_out = (int)((int64_t)F + before_all < a.n_blocks ? F + before_all : a.n_blocks);
+  *free_out = (int)((int64_t)F + before_all < a.n_blocks ? F + before_all : a.n_blocks);
+}
+
+SDV_DEV void commit_out(const CommitArgs& a, int r, const Committed& c) {
+  a.seq_out[r] = c.len;
+  a.n_new[r] = c.n_new;
+  if (a.x0_out) a.x0_out[r] = c.n_new ? a.out_tokens[(int64_t)r * a.q_max + c.acc] : a.x0[r];
+  if (c.bad && a.status) a.status[r] |= SD_ST_BAD_INPUT;
+}
+
+// The blocks of a request back to the free list, by one wave.
+SDV_DEV void give_back(const CommitArgs& a, int r, int kept, int give, int to) {
+  const int32_t* table = a.table + (int64_t)r * a.max_blocks + kept;
+  for (int i = threadIdx.x & 63; i < give; i += 64)
+    if ((int64_t)to + i < a.n_blocks) a.free_list[to + i] = table[i];
+}
+
+// One launch: every workgroup repeats the scan and keeps the requests of its
+// waves.  No output may be an input unless the grid is one workgroup (the
+// status may: its new bit is not read).
+template <int kItems>
+__global__ __launch_bounds__(kFillThreads) void k_commit_all(CommitArgs a) {
+  __shared__ uint64_t part[kScanWaves];
+  __shared__ int kept[kOneLaunchRequests], give[kOneLaunchRequests], to[kOneLaunchRequests];
+  int left;
+  commit_scan<kItems>(a, part, &left, [&](int r, const Committed& c) {
+    kept[r] = c.kept;
+    give[r] = c.give;
+    to[r] = c.to;
+    if (r % gridDim.x == blockIdx.x) commit_out(a, r, c);
+  });
+  __syncthreads();
+  for (int r = blockIdx.x + (threadIdx.x >> 6) * gridDim.x; r < a.R; r += gridDim.x * (kFillThreads / 64))
+    if (give[r]) give_back(a, r, kept[r], give[r], to[r]);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.free_out = left;
+}
+
+// Two launches, for more requests or outputs in the place of inputs.
+template <int kItems>
+__global__ __launch_bounds__(kScanThreads) void k_commit_scan(CommitArgs a) {
+  __shared__ uint64_t part[kScanWaves];
+  int left;
+  commit_scan<kItems>(a, part, &left, [&](int r, const Committed& c) {
+    a.ws[3 * r] = c.kept;
+    a.ws[3 * r + 1] = c.give;
+    a.ws[3 * r + 2] = c.to;
+    commit_out(a, r, c);
+  });
+  __syncthreads();   // free_out may be free_count, which every thread has read now
+  if (threadIdx.x == 0) *a.free_out = left;
 }
 
 __global__ __launch_bounds__(kFillThreads) void k_commit_move(CommitArgs a) {
-  const int r = blockIdx.x;
-  const int kept = a.ws[3 * r], give = a.ws[3 * r + 1], to = a.ws[3 * r + 2];
-  for (int i = threadIdx.x; i < give; i += kFillThreads)
-    if ((int64_t)to + i < a.n_blocks) a.free_list[to + i] = a.table[(int64_t)r * a.max_blocks + kept + i];
+  const int r = blockIdx.x * (kFillThreads / 64) + (threadIdx.x >> 6);
+  if (r < a.R) give_back(a, r, a.ws[3 * r], a.ws[3 * r + 1], a.ws[3 * r + 2]);
 }
 
 }  // namespace
@@ -301,9 +528,18 @@ extern "C" int sd_slot_reserve(hipStream_t stream, int R, int q_max, int block_s
   a.max_rows = max_rows;
   a.padded = padded;
   a.ld_tokens = ld_tokens;
-  SDV_TRY_LAUNCH(sdv::launch(k_reserve_scan, dim3(1), dim3(kScanThreads), 0, stream, a));
-  SDV_TRY_LAUNCH(sdv::launch(k_reserve_rows, dim3((max_rows + kFillThreads - 1) / kFillThreads),
-                             dim3(kFillThreads), 0, stream, a));
+  // a thread per row and, as far as the grid goes, a wave per request
+  const int row_wgs = (max_rows + kFillThreads - 1) / kFillThreads, req_wgs = (R + 3) / 4;
+  const unsigned wgs = (unsigned)(row_wgs > req_wgs ? row_wgs : req_wgs);
+  const bool over = ell_out == ell || free_left == free_count;   // an output in an input's place
+  if (R <= kOneLaunchRequests && (!over || wgs == 1)) {
+    const auto k = R <= kFillThreads ? k_reserve_all<1> : (R <= 2 * kFillThreads ? k_reserve_all<2> : k_reserve_all<4>);
+    SDV_TRY_LAUNCH(sdv::launch(k, dim3(wgs < kOneLaunchGrid ? wgs : kOneLaunchGrid), dim3(kFillThreads), 0, stream, a));
+    return SD_OK;
+  }
+  SDV_TRY_LAUNCH(sdv::launch(R <= kScanThreads ? k_reserve_scan<1> : k_reserve_scan<4>, dim3(1),
+                             dim3(scan_threads(R)), 0, stream, a));
+  SDV_TRY_LAUNCH(sdv::launch(k_reserve_rows, dim3(wgs), dim3(kFillThreads), 0, stream, a));
   return SD_OK;
 }
 
@@ -320,9 +556,9 @@ extern "C" int sd_slot_commit(hipStream_t stream, int R, int q_max, int block_si
                               void* workspace, size_t workspace_bytes) {
   if (R < 0 || q_max < 1 || block_size < 1 || max_blocks < 1 || n_blocks < 0) return SD_EINVAL;
   const long long lim = 0x7FFFFFFFLL - kFillThreads;
-  if ((long long)block_size * max_blocks > lim || (long long)R * max_blocks > lim || (long long)R * q_max > lim)
+  if ((long long)block_size * max_blocks > lim || (long long)R * max_blocks + n_blocks > lim ||
+      (long long)R * q_max > lim)
     return SD_EUNSUPPORTED;
-  if ((long long)R * kFillThreads > 0xFFFFFFFFLL) return SD_EUNSUPPORTED;  // work-items of one launch
   if (R == 0) return SD_OK;
   if (!seq_len || !ell || !n_accepted || !block_table || (n_blocks > 0 && !free_list) || !free_count ||
       !seq_len_out || !n_new || !free_count_out)
@@ -352,7 +588,15 @@ extern "C" int sd_slot_commit(hipStream_t stream, int R, int q_max, int block_si
   a.bs = block_size;
   a.max_blocks = max_blocks;
   a.n_blocks = n_blocks;
-  SDV_TRY_LAUNCH(sdv::launch(k_commit_scan, dim3(1), dim3(kScanThreads), 0, stream, a));
-  SDV_TRY_LAUNCH(sdv::launch(k_commit_move, dim3(R), dim3(kFillThreads), 0, stream, a));
+  const unsigned wgs = (unsigned)((R + kCommitRequests - 1) / kCommitRequests);
+  const bool over = seq_len_out == seq_len || free_count_out == free_count || (x0_out && x0_out == x0);
+  if (R <= kOneLaunchRequests && (!over || wgs == 1)) {
+    const auto k = R <= kFillThreads ? k_commit_all<1> : (R <= 2 * kFillThreads ? k_commit_all<2> : k_commit_all<4>);
+    SDV_TRY_LAUNCH(sdv::launch(k, dim3(wgs), dim3(kFillThreads), 0, stream, a));
+    return SD_OK;
+  }
+  SDV_TRY_LAUNCH(sdv::launch(R <= kScanThreads ? k_commit_scan<1> : k_commit_scan<4>, dim3(1),
+                             dim3(scan_threads(R)), 0, stream, a));
+  SDV_TRY_LAUNCH(sdv::launch(k_commit_move, dim3((R + 3) / 4), dim3(kFillThreads), 0, stream, a));
   return SD_OK;
 }

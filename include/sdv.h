@@ -551,8 +551,8 @@ int sd_token_counts(hipStream_t stream, int R, int V, const int32_t* tokens, lon
  *   x0_out and free_count_out may be seq_len, x0 and free_count.  The entries
  *   of block_table stay as they are.
  *
- * block_size * max_blocks, R * q_max, R * max_blocks and max_rows stay below
- * 2^31 - 256; workspaces of sd_slot_*_workspace_size(R) bytes.
+ * block_size * max_blocks, R * q_max, R * max_blocks (sd_slot_commit: +
+ * n_blocks) and max_rows are at most 2^31 - 257; workspaces of sd_slot_*_workspace_size(R) bytes.
  */
 size_t sd_slot_reserve_workspace_size(int R);
 int sd_slot_reserve(hipStream_t stream, int R, int q_max, int block_size, int max_blocks,
