@@ -174,6 +174,13 @@ __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
   unsigned seen = 0;
   if (pen && a.seen && mine) seen = ((const uint8_t*)(a.seen + (int64_t)srow * a.ld_seen))[v0 >> 3];
 
+  // a draft before the row counts as written; most chunks hold none of them
+  const int32_t* const drafts = pen && a.draft ? a.draft + (int64_t)r * a.gmax : nullptr;
+  bool here = false;
+  if (drafts)
+    for (int i = tid; i < i1 - 1; i += kShapeThreads) here |= (unsigned)drafts[i] / kShapeChunk == (unsigned)ch;
+  const int32_t* const draft = __ballot(here) ? drafts : nullptr;
+
   int bad = 0;
   float bias[kVecTokens] = {};
   unsigned biased = 0;
@@ -197,6 +204,8 @@ __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
       }
     }
   }
+  // in place, most chunks of a request without a mask hold nothing to change
+  if (!COPY && !mask && !draft && !tell && !__ballot(seen | biased)) return;
   float c[kVecTokens] = {};   // counts up to 2^24 are exact
   if (seen && a.counts) {
     const int4* p = (const int4*)(a.counts + (int64_t)srow * a.ld_counts + v0);
@@ -205,8 +214,6 @@ __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
 #pragma unroll
     for (int e = 0; e < kVecTokens; ++e) c[e] = (seen >> e) & 1 ? (float)k[e] : 0.0f;
   }
-  // a draft before the row counts as written
-  const int32_t* draft = pen && a.draft ? a.draft + (int64_t)r * a.gmax : nullptr;
   auto count = [&](int t) {
 #pragma unroll
     for (int e = 0; e < kVecTokens; ++e)
@@ -272,8 +279,8 @@ __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
     }
   }
   if (tell) {
-    if (draft)
-      for (int i = tid; i < n - 1; i += kShapeThreads) bad |= draft[i] < 0 || draft[i] >= a.V;
+    if (drafts)
+      for (int i = tid; i < n - 1; i += kShapeThreads) bad |= drafts[i] < 0 || drafts[i] >= a.V;
     bad = __syncthreads_or(bad);
     if (tid == 0) a.status[r] = bad ? SD_ST_BAD_TOKEN : 0;
   }
