@@ -108,6 +108,85 @@ struct Oct<false> {
   }
 };
 
+// What a request asks for, and whether its device-side arguments are in range.
+struct Request {
+  int n;       // rows
+  int row0, srow, m0;
+  int64_t b0, b1;
+  float rep, freq, pres;
+  bool pen, ok;
+};
+SDV_DEV Request read_request(const ShapeArgs& a, int r) {
+  Request q;   // requested together
+  q.n = min(a.ell[r], a.gmax) + 1;
+  q.row0 = a.row0[r];
+  q.rep = a.rep ? a.rep[r] : 1.0f;
+  q.freq = a.freq ? a.freq[r] : 0.0f;
+  q.pres = a.pres ? a.pres[r] : 0.0f;
+  q.srow = a.slot ? a.slot[r] : r;
+  q.m0 = a.mask_row0 ? a.mask_row0[r] : -1;
+  q.b0 = a.bias_off ? a.bias_off[r] : 0;
+  q.b1 = a.bias_off ? a.bias_off[r + 1] : 0;
+  const float inf = __builtin_huge_valf();
+  q.pen = q.rep != 1.0f || q.freq != 0.0f || q.pres != 0.0f;
+  q.ok = q.row0 >= 0 && (int64_t)q.row0 + q.n <= a.n_rows;
+  q.ok = q.ok && q.rep > 0.0f && q.rep < inf && fabsf(q.freq) < inf && fabsf(q.pres) < inf;
+  q.ok = q.ok && (!q.pen || (q.srow >= 0 && q.srow < a.n_slots));
+  q.ok = q.ok && (q.m0 < 0 || (int64_t)q.m0 + q.n <= a.n_mask_rows);
+  q.ok = q.ok && q.b0 >= 0 && q.b0 <= q.b1 && q.b1 <= a.n_bias;
+  return q;
+}
+
+// What a lane holds for its eight tokens v0..v0+7.
+struct Tokens {
+  unsigned seen = 0;               // by the state, then by the drafts so far
+  float c[kVecTokens] = {};        // written how often; up to 2^24 exact
+  unsigned biased = 0;
+  float bias[kVecTokens] = {};
+
+  SDV_DEV void read_counts(const ShapeArgs& a, int srow, int v0) {
+    if (!seen || !a.counts) return;
+    const int4* p = (const int4*)(a.counts + (int64_t)srow * a.ld_counts + v0);
+    const int4 p0 = p[0], p1 = p[1];
+    const int k[kVecTokens] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+    for (int e = 0; e < kVecTokens; ++e) c[e] = (seen >> e) & 1 ? (float)k[e] : 0.0f;
+  }
+  SDV_DEV void write(int t, int v0) {   // token t counts as written
+#pragma unroll
+    for (int e = 0; e < kVecTokens; ++e)
+      if (t == v0 + e) {
+        c[e] += 1.0f;
+        seen |= 1u << e;
+      }
+  }
+  // The terms of the tokens in `hit`, of which those in `met` are seen.
+  template <typename O>
+  SDV_DEV void apply(const Request& q, unsigned hit, unsigned met, O& x) const {
+#pragma unroll
+    for (int e = 0; e < kVecTokens; ++e)
+      if ((hit >> e) & 1) {
+        float y = x.get(e);
+        if ((met >> e) & 1) {
+          y = y > 0.0f ? y / q.rep : y * q.rep;
+          y -= q.freq * c[e];
+          if (c[e] > 0.0f) y -= q.pres;
+        }
+        if ((biased >> e) & 1) y += bias[e];
+        x.set(e, y);
+      }
+  }
+};
+
+// The request's status: a draft or a bias entry outside the vocabulary.
+SDV_DEV void report(const ShapeArgs& a, int r, const int32_t* drafts, int n, int bad) {
+  const int lane = threadIdx.x;
+  if (drafts)
+    for (int i = lane; i < n - 1; i += kShapeThreads) bad |= drafts[i] < 0 || drafts[i] >= a.V;
+  const bool any = __ballot(bad != 0) != 0;
+  if (lane == 0) a.status[r] = any ? SD_ST_BAD_TOKEN : 0;
+}
+
 // One wave per (request, chunk of 512 tokens, group of rows); a lane owns
 // eight consecutive tokens in every row of the group, so the request's state
 // is read once and stays in registers while the rows stream past.  NT: a
@@ -118,29 +197,15 @@ __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
   __shared__ int last[kShapeChunk];   // 1 + index of a token's last bias entry
   const int r = blockIdx.x / a.n_ch, ch = blockIdx.x % a.n_ch;
   const int tid = threadIdx.x;
-  // everything that describes the request is requested together
-  const int n = min(a.ell[r], a.gmax) + 1;   // rows
-  const int row0 = a.row0[r];
-  const float rep = a.rep ? a.rep[r] : 1.0f;
-  const float freq = a.freq ? a.freq[r] : 0.0f;
-  const float pres = a.pres ? a.pres[r] : 0.0f;
-  const int srow = a.slot ? a.slot[r] : r;
-  const int m0 = a.mask_row0 ? a.mask_row0[r] : -1;
-  const int64_t b0 = a.bias_off ? a.bias_off[r] : 0, b1 = a.bias_off ? a.bias_off[r + 1] : 0;
+  const Request q = read_request(a, r);
+  const int n = q.n, row0 = q.row0, m0 = q.m0;
   const int i0 = blockIdx.y * a.group, i1 = min(n, i0 + a.group);
   const bool tell = ch == 0 && i0 == 0;      // this wave reports the request's status
   if (i0 >= i1) {
     if (tell && tid == 0) a.status[r] = 0;
     return;
   }
-  const float inf = __builtin_huge_valf();
-  const bool pen = rep != 1.0f || freq != 0.0f || pres != 0.0f;
-  bool ok = row0 >= 0 && (int64_t)row0 + n <= a.n_rows;
-  ok = ok && rep > 0.0f && rep < inf && fabsf(freq) < inf && fabsf(pres) < inf;
-  ok = ok && (!pen || (srow >= 0 && srow < a.n_slots));
-  ok = ok && (m0 < 0 || (int64_t)m0 + n <= a.n_mask_rows);
-  ok = ok && b0 >= 0 && b0 <= b1 && b1 <= a.n_bias;
-  if (!ok) {   // uniform over the request's waves: none of its rows is written
+  if (!q.ok) {   // uniform over the request's waves: none of its rows is written
     if (tell && tid == 0) a.status[r] = SD_ST_BAD_INPUT;
     return;
   }
@@ -171,26 +236,24 @@ __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
     fetch_mask(0);
     fetch_all(0);
   }
-  unsigned seen = 0;
-  if (pen && a.seen && mine) seen = ((const uint8_t*)(a.seen + (int64_t)srow * a.ld_seen))[v0 >> 3];
+  Tokens tk;
+  if (q.pen && mine) tk.seen = ((const uint8_t*)(a.seen + (int64_t)q.srow * a.ld_seen))[v0 >> 3];
 
   // a draft before the row counts as written; most chunks hold none of them
-  const int32_t* const drafts = pen && a.draft ? a.draft + (int64_t)r * a.gmax : nullptr;
+  const int32_t* const drafts = q.pen && a.draft ? a.draft + (int64_t)r * a.gmax : nullptr;
   bool here = false;
   if (drafts)
     for (int i = tid; i < i1 - 1; i += kShapeThreads) here |= (unsigned)drafts[i] / kShapeChunk == (unsigned)ch;
   const int32_t* const draft = __ballot(here) ? drafts : nullptr;
 
   int bad = 0;
-  float bias[kVecTokens] = {};
-  unsigned biased = 0;
-  if (b1 > b0) {
+  if (q.b1 > q.b0) {
 #pragma unroll
     for (int e = 0; e < kVecTokens; ++e) last[e * kShapeThreads + tid] = 0;
     __syncthreads();
-    const int nb = (int)(b1 - b0);
+    const int nb = (int)(q.b1 - q.b0);
     for (int i = tid; i < nb; i += kShapeThreads) {
-      const int t = a.bias_tok[b0 + i];
+      const int t = a.bias_tok[q.b0 + i];
       if (t < 0 || t >= a.V) bad = 1;
       else if (t / kShapeChunk == ch) atomicMax(&last[t % kShapeChunk], i + 1);
     }
@@ -199,31 +262,16 @@ __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
     for (int e = 0; e < kVecTokens; ++e) {
       const int i = last[tid * kVecTokens + e];
       if (i > 0) {
-        bias[e] = a.bias_val[b0 + i - 1];
-        biased |= 1u << e;
+        tk.bias[e] = a.bias_val[q.b0 + i - 1];
+        tk.biased |= 1u << e;
       }
     }
   }
   // in place, most chunks of a request without a mask hold nothing to change
-  if (!COPY && !mask && !draft && !tell && !__ballot(seen | biased)) return;
-  float c[kVecTokens] = {};   // counts up to 2^24 are exact
-  if (seen && a.counts) {
-    const int4* p = (const int4*)(a.counts + (int64_t)srow * a.ld_counts + v0);
-    const int4 p0 = p[0], p1 = p[1];
-    const int k[kVecTokens] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-#pragma unroll
-    for (int e = 0; e < kVecTokens; ++e) c[e] = (seen >> e) & 1 ? (float)k[e] : 0.0f;
-  }
-  auto count = [&](int t) {
-#pragma unroll
-    for (int e = 0; e < kVecTokens; ++e)
-      if (t == v0 + e) {
-        c[e] += 1.0f;
-        seen |= 1u << e;
-      }
-  };
+  if (!COPY && !mask && !draft && !tell && !__ballot(tk.seen | tk.biased)) return;
+  tk.read_counts(a, q.srow, v0);
   if (draft)
-    for (int i = 0; i < i0; ++i) count(draft[i]);
+    for (int i = 0; i < i0; ++i) tk.write(draft[i], v0);
 
   for (int i = 0; i < m_all; i += kRows) {
     if (NT) fetch_mask(i);
@@ -231,7 +279,7 @@ __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
     unsigned met[kRows];
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
-      met[k] = k ? met[k - 1] : seen;
+      met[k] = k ? met[k - 1] : tk.seen;
       if (draft && i + k > 0 && i + k < m_all) {
         const int t = draft[i0 + i + k - 1];
         if ((t >> 3) == (v0 >> 3)) met[k] |= 1u << (t & 7);
@@ -242,7 +290,7 @@ __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
     unsigned touched[kRows];
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
-      touched[k] = met[k] | biased | (allowed[k] ^ 0xFFu);
+      touched[k] = met[k] | tk.biased | (allowed[k] ^ 0xFFu);
       if (!COPY && __popcll(__ballot(touched[k] != 0)) >= kWholeLanes) touched[k] = 1;
     }
     if (NT) {
@@ -254,22 +302,9 @@ __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
       if (i + k >= m_all) break;
-      if (draft && i + k > 0 && met[k]) count(draft[i0 + i + k - 1]);
-      const unsigned hit = (met[k] | biased) & allowed[k];
-      if (hit) {
-#pragma unroll
-        for (int e = 0; e < kVecTokens; ++e)
-          if ((hit >> e) & 1) {
-            float y = x[k].get(e);
-            if ((met[k] >> e) & 1) {
-              y = y > 0.0f ? y / rep : y * rep;
-              y -= freq * c[e];
-              if (c[e] > 0.0f) y -= pres;
-            }
-            if ((biased >> e) & 1) y += bias[e];
-            x[k].set(e, y);
-          }
-      }
+      if (draft && i + k > 0 && met[k]) tk.write(draft[i0 + i + k - 1], v0);
+      const unsigned hit = (met[k] | tk.biased) & allowed[k];
+      if (hit) tk.apply(q, hit, met[k], x[k]);
       if (allowed[k] != 0xFFu) x[k].keep(allowed[k]);
       if (COPY || touched[k]) x[k].template store<NT>(dst + (i + k) * a.ld_bytes);
     }
@@ -278,12 +313,7 @@ __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
       fetch_all(i + kRows);
     }
   }
-  if (tell) {
-    if (drafts)
-      for (int i = tid; i < n - 1; i += kShapeThreads) bad |= drafts[i] < 0 || drafts[i] >= a.V;
-    bad = __syncthreads_or(bad);
-    if (tid == 0) a.status[r] = bad ? SD_ST_BAD_TOKEN : 0;
-  }
+  if (tell) report(a, r, drafts, n, bad);
 }
 
 // ---------------------------------------------------------------------------

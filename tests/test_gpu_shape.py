@@ -61,11 +61,15 @@ def _case(R, gmax, V, dtype=torch.bfloat16, pad=0, seed=0, packed=False, draft=T
     return c
 
 
-def _gpu(c, in_place=False, stream=None, out=None):
+def _gpu(c, in_place=False, stream=None, out=None, raw=False, ld=None):
     i32 = lambda a: None if a is None else torch.as_tensor(np.ascontiguousarray(a), dtype=torch.int32).to(DEV)  # noqa: E731
     f32 = lambda a: None if a is None else torch.as_tensor(a).to(DEV)  # noqa: E731
     V, w = c["V"], (c["V"] + 31) // 32 + c["wide"]
     x = c["x"].to(DEV)
+    if ld is not None:   # the same rows further apart
+        wide = torch.full((x.shape[0], ld), 7.0, dtype=x.dtype, device=DEV)
+        wide[:, :V] = x[:, :V]
+        x = wide
     cnt = np.full((c["counts"].shape[0], V + 4 * c["wide"]), 77)
     cnt[:, :V] = c["counts"]
     pen = c["rep"] is not None or c["freq"] is not None
@@ -86,6 +90,8 @@ def _gpu(c, in_place=False, stream=None, out=None):
         mask=None if c["allowed"] is None else i32(OS.pack_bits(c["allowed"], w)), mask_row0=i32(c["m0"]),
         out=out, stream=stream)
     torch.cuda.synchronize()
+    if raw:
+        return got
     return to_np(got["logits"]).astype(np.float64), to_np(got["status"])
 
 
@@ -144,6 +150,33 @@ def test_sizes(R, gmax, V, pad, dtype, in_place):
                                 dict(hist=4000), dict(bias=2500), dict(ells=[-1, -1, -1, -1])])
 def test_terms(kw, in_place):
     _check(_case(4, 5, 5000, seed=len(str(kw)), **kw), in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kw", [dict(), dict(mask=False), dict(mask=False, bias=0), dict(mask=False, bias=900),
+                                dict(mask=False, rep=False, fp=False), dict(mask=False, draft=False, hist=3000),
+                                dict(mask=False, fp=False), dict(rep=False, fp=False)])
+def test_batches_past_the_cache(kw, dtype, in_place):
+    """Batches that do not fit the last-level cache take other kernels: with
+    rows far apart they give the bits of the same rows packed (checked against
+    the oracle), and leave the rest of the rows alone."""
+    c = _case(9, 7, 17000, dtype, seed=21, packed=True, extra=1, wide=1, ells=[7, 7, 0, 3, -1, 7, 5, 6, 7], **kw)
+    c["allowed"] = None if c["allowed"] is None else c["allowed"].copy()
+    if c["allowed"] is not None:
+        c["allowed"][:2] = True
+        c["allowed"][8] = False
+    _check(c, in_place)
+    near = _gpu(c, in_place, raw=True)
+    rows, esize = c["x"].shape[0], 2 if dtype is torch.bfloat16 else 4
+    ld = (140 << 20) // (72 * esize * (1 if in_place else 2)) // 8 * 8
+    far = _gpu(c, in_place, raw=True, ld=ld)
+    assert torch.equal(near["status"], far["status"])
+    V = c["V"]
+    a, b = near["logits"][:, :V].contiguous(), far["logits"][:, :V].contiguous()
+    word = torch.int16 if esize == 2 else torch.int32
+    assert torch.equal(a.view(word), b.view(word))
+    assert (far["logits"][:, V:] == (7.0 if in_place else 123.0)).all() and far["logits"].shape == (rows, ld)
 
 
 @pytest.mark.parametrize("in_place", [False, True])
