@@ -16,9 +16,16 @@ namespace {
 constexpr int kShapeThreads = 64;
 constexpr int kVecTokens = 8;                              // tokens per thread: one mask byte
 constexpr int kShapeChunk = kShapeThreads * kVecTokens;    // tokens per workgroup
-constexpr long long kFullWaves = 8192;   // resident waves of the chip at this kernel's registers
-constexpr int kWholeLanes = 32;
+// Resident waves of the chip at this kernel's registers: a batch with fewer
+// (request, chunk) waves splits its rows over more (64 requests, V = 32000:
+// 14.9 us split in two, 20.8 us unsplit; 4 requests, V = 1000: 4.0 and 8.5 us;
+// a batch that fills the chip anyway loses 100 us of 460 by a split in two).
+constexpr long long kFullWaves = 8192;
+// Beyond this the rows do not stay in the 256 MB last-level cache: they are
+// streamed past it and wait for their masks (512 requests, V = 151936: 461 us
+// streamed, 548 us not; 64 requests, V = 32000: 17.1 and 15.9 us).
 constexpr double kCacheBytes = 128 << 20;
+constexpr int kWholeLanes = 32;   // (grammars in place: 64 us, 72 us vector by vector)
 
 struct ShapeArgs {
   const char* logits;
@@ -187,13 +194,25 @@ SDV_DEV void report(const ShapeArgs& a, int r, const int32_t* drafts, int n, int
   if (lane == 0) a.status[r] = any ? SD_ST_BAD_TOKEN : 0;
 }
 
-// One wave per (request, chunk of 512 tokens, group of rows); a lane owns
-// eight consecutive tokens in every row of the group, so the request's state
-// is read once and stays in registers while the rows stream past.  NT: a
-// batch that does not fit the last-level cache.
+// l -> the row's logit with the request's terms (see read_request, Tokens):
+// elementwise, so bound by the bytes of the rows.  One wave per (request,
+// chunk of 512 tokens, group of rows); a lane owns eight consecutive tokens
+// (16 bytes of bf16, one byte of a bitmap) in every row of the group, so the
+// request's state is read once and stays in registers while the rows stream
+// past, and no other lane's data is needed: workgroups of one wave were
+// fastest (448 us, 455 us with two and 481 us with four waves).  NT: a batch
+// that does not fit the last-level cache.
+// Measured: 512 requests with up to 17 rows each, V = 151936 bf16, out of
+// place, every term: 430 us for 2.46 GB of memory traffic, 5.7 TB/s (a plain
+// copy reaches 4.9); grammars in place, 128 requests, V = 129280: 63.5 us,
+// 0.30 GB, 4.7 TB/s (partial lines); penalties alone in place, 512 requests:
+// 251 us, half of what it takes out of place.
 template <bool BF16, bool NT, bool COPY>
 __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
-  constexpr int kRows = NT ? (COPY ? 2 : 4) : 1;   // rows whose loads are issued together
+  // rows whose loads are issued together (large batch out of place: 1: 469 us,
+  // 2: 463 us, 4: 486 us; in place 2: 70 us, 4: 67 us; 64 requests at V =
+  // 32000 1: 14.9 us, 2: 15.9 us)
+  constexpr int kRows = NT ? (COPY ? 2 : 4) : 1;
   __shared__ int last[kShapeChunk];   // 1 + index of a token's last bias entry
   const int r = blockIdx.x / a.n_ch, ch = blockIdx.x % a.n_ch;
   const int tid = threadIdx.x;
@@ -345,8 +364,8 @@ SDV_DEV bool count_row(const CountArgs& a, int r, int64_t* at, int* n, int* srow
 
 constexpr int kCountThreads = 256;
 
-// Lists of a few tokens (a step's accepted ones) without a reset: atomics on
-// the state, whose order does not matter to whole numbers.
+// Short lists (a step's accepted tokens) without a reset: atomics on the
+// state, whose order does not matter to whole numbers.
 __global__ __launch_bounds__(kCountThreads) void k_count_add(CountArgs a) {
   const int r = blockIdx.x;
   int64_t at;
@@ -378,22 +397,29 @@ __global__ __launch_bounds__(kCountThreads) void k_count_clear(CountArgs a) {
     for (int v = first; v < a.V; v += step) a.counts[(int64_t)srow * a.ld_counts + v] = 0;
 }
 
-// With resets a state row is written whole, so one workgroup owns a range of
-// the vocabulary in one state row: it counts in LDS the tokens of every list
-// entered into that row, then writes the range once, coalesced.  A word of LDS
-// holds a token's count and, in its top bit, that it was seen.  The lists are
-// read once per range and are bound by the instructions of the filter, short
-// ones by the writing.  Measured: 96 lists of up to 131072 tokens, V = 151936:
-// 34 us, 252 us with a clearing pass and atomics on the state (1.8 ms where
-// half of a list is one token); 256 lists of at most 100: 33 us, 4.9 TB/s.
+// With resets, where a state row is written whole, and for long lists one
+// workgroup owns a range of the vocabulary in one state row: it counts in LDS
+// the tokens of every list entered into that row, then writes the range once,
+// coalesced (without a reset: adds to what the lists touch).  A word of LDS
+// holds a token's count and, in its top bit, that it was seen.  Every range
+// reads the whole list; long lists are bound by the instructions of that
+// filter (and wait for the ranges of the frequent tokens), short ones by the
+// writing.  Measured at V = 151936: 96 lists of up to 131072 tokens 33 us
+// (252 us with a clearing pass and atomics on the state, 1.8 ms where half of
+// a list is one token); 256 lists of at most 100 tokens 33 us, 4.9 TB/s.
 constexpr int kOwnThreads = 1024;
-constexpr int kOwnLoads = 8;
+constexpr int kOwnLoads = 8;             // 4: 39 us, 16: 34 us for the 96 lists
 constexpr int kOwnMaxChunk = 32768;      // 128 KB of the 160 KB of LDS
 // Lists below this mean length are entered in half as large ranges, two
-// workgroups per CU (256 short lists: 33 against 37 us; the long ones above:
-// 36.5 against 34.5 us).
+// workgroups per CU (256 short lists: 33 against 37 us; the 96 long ones
+// above: 36.5 against 34.5 us).
 constexpr int kOwnLongList = 8192;
-constexpr int kOwnMaxRequests = 4096;    // above, the search for shared rows outgrows the counting
+// Without a reset, from this mean length on (64 lists of 2048 tokens: atomics
+// 12.7 us, ranges 15.0 us; of 8192 tokens: 48 and 23 us).
+constexpr int kOwnMinList = 4096;
+// The search for shared state rows grows with the square of the requests
+// (8192 requests at V = 4000: 71 us, 38 us cleared first and added to).
+constexpr int kOwnMaxRequests = 4096;
 constexpr uint32_t kSeenBit = 0x80000000u;
 
 // Enter n tokens into the workgroup's range: MARK sets the seen bit, else the
@@ -402,8 +428,8 @@ template <bool MARK>
 SDV_DEV void enter_tokens(uint32_t* cell, const int32_t* tokens, int n, int v0, int width) {
   const int tid = threadIdx.x;
   auto one = [&](int tok) {
-    const unsigned t = (unsigned)tok - (unsigned)v0;
-    if (tok < 0 || t >= (unsigned)width) return;
+    const unsigned t = (unsigned)tok - (unsigned)v0;   // a negative token is past every range
+    if (t >= (unsigned)width) return;
     // a stretch of one token would queue the wave's lanes at one word
     const unsigned t0 = __builtin_amdgcn_readfirstlane(t);
     const uint64_t lanes = __ballot(true);
@@ -449,7 +475,7 @@ __global__ __launch_bounds__(kOwnThreads) void k_count_own(CountArgs a) {
   if (!ok) return;
   if (tid == 0) {
     shared_row = 0;
-    reset_row = a.reset[r] != 0;
+    reset_row = a.reset && a.reset[r];
   }
   for (int v = tid; v < a.chunk; v += kOwnThreads) cell[v] = 0;
   __syncthreads();
@@ -461,7 +487,7 @@ __global__ __launch_bounds__(kOwnThreads) void k_count_own(CountArgs a) {
         int n_q, s_q;
         if (count_row(a, q, &at_q, &n_q, &s_q)) {
           atomicOr(&shared_row, q < r ? 2 : 1);
-          if (a.reset[q]) reset_row = 1;
+          if (a.reset && a.reset[q]) reset_row = 1;
         }
       }
   __syncthreads();
@@ -628,8 +654,8 @@ extern "C" int sd_token_counts(hipStream_t stream, int R, int V, const int32_t* 
     const long long fill = (2048 + R - 1) / R, need = (work + each - 1) / each;
     return (unsigned)(need < 1 ? 1 : (need < fill ? need : fill));
   };
-  if (reset && R <= kOwnMaxRequests) {
-    const long long mean = (start ? n_tokens : (long long)R * width) / R;
+  const long long mean = (start ? n_tokens : (long long)R * width) / R;
+  if ((reset || mean >= kOwnMinList) && R <= kOwnMaxRequests) {
     const int most = mean < kOwnLongList ? kOwnMaxChunk / 2 : kOwnMaxChunk;
     a.chunk = V < most ? (V + 63) / 64 * 64 : most;
     const int n_ch = (V + a.chunk - 1) / a.chunk;

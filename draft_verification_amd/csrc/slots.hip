@@ -6,6 +6,11 @@
 // reserved for all of them and cut back afterwards to what was accepted
 // (LightSpec article, system section).  Neither may wait for the host, so
 // both steps are prefix sums over the requests on the device.
+//
+// They read and write some 60 bytes per request and 20 per row, so a verify
+// batch is bound by its chain of dependent loads (count and lengths, scan,
+// blocks, rows: 3.7 us for 4 requests), and long pieces of prompts by the
+// rows' stores (640 k rows, 13 MB: 9 us).
 #include "sdv_host.h"
 #include "verify_common.h"
 
@@ -14,9 +19,15 @@ namespace {
 constexpr int kScanThreads = 1024;
 constexpr int kScanWaves = kScanThreads / 64;
 constexpr int kFillThreads = 256;
-constexpr int kOneLaunchRequests = 1024;  // requests whose scan a workgroup keeps in LDS
-constexpr int kOneLaunchGrid = 1024;      // workgroups that repeat the scan
-constexpr int kCommitRequests = 4;        // requests per workgroup of k_commit_all
+// Up to these requests every workgroup repeats the scan and keeps it in LDS:
+// one launch (512 requests with up to 17 rows: 6.0 us, 8.0 us in two launches;
+// 4 requests: 3.7 and 4.3 us; commit 4.8 and 5.9 us, 2.8 and 3.7 us).
+constexpr int kOneLaunchRequests = 1024;
+constexpr int kOneLaunchGrid = 1024;      // (640 k rows: 9.0 us, 15.6 us with 256 workgroups)
+constexpr int kCommitRequests = 4;        // per workgroup (512 requests: 5.9 us, 8: 6.5 us, 16: 6.8 us)
+// Requests per thread of such a scan: 1 up to 256 requests, 2 up to 512, else
+// 4, so that one pass covers them all (reserve, 1 / 2 / 4 per thread: 64
+// requests 5.3 / 5.5 / 5.9 us, 512: 7.2 / 6.1 / 6.4 us, 1024: 7.1 / 5.7 / 5.2 us).
 
 // As many waves as the requests fill, up to a workgroup.
 unsigned scan_threads(int R) { return R >= kScanThreads ? kScanThreads : (unsigned)(R + 63) / 64 * 64; }

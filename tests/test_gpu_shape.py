@@ -367,6 +367,16 @@ def test_counts_of_one_row_shared_by_requests():
     _counts_check([g.integers(0, 64, 500) for _ in range(6)], 64, slot=[2, 2, 0, 2, 0, 2], reset=[1, 0, 0, 1, 0, 0])
 
 
+def test_counts_of_long_lists_added():
+    """Long lists without a reset, two of them into one state row."""
+    g = np.random.default_rng(8)
+    V = 40000
+    lists = [(V * g.random(k) ** 2).astype(int) for k in (9000, 30000, 8193, 0, 4100)] + [np.full(20000, 32767)]
+    lists[1][100:200] = [-1, V] * 50
+    _counts_check(lists, V, prompt=[0, 20000, 8192, 0, 9000, 5], slot=[4, 1, 4, 2, 0, 3], extra=1)
+    _counts_check(lists, V, slot=[4, 1, 4, 2, 0, 3], with_counts=False)
+
+
 def test_counts_of_very_many_requests():
     g = np.random.default_rng(6)
     R = 4100
