@@ -454,10 +454,10 @@ SDV_DEV void enter_tokens(uint32_t* cell, const int32_t* tokens, int n, int v0, 
 #pragma unroll
     for (int k = 0; k < kOwnLoads; ++k) one(tok[k]);
   }
-  for (int i = full + tid; i < n; i += 4 * kOwnThreads) {
+  for (int64_t i = full + tid; i < n; i += 4 * kOwnThreads) {
     int tok[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) tok[k] = n - i > k * kOwnThreads ? tokens[i + k * kOwnThreads] : -1;
+    for (int k = 0; k < 4; ++k) tok[k] = i + k * kOwnThreads < n ? tokens[i + k * kOwnThreads] : -1;
 #pragma unroll
     for (int k = 0; k < 4; ++k) one(tok[k]);
   }
@@ -568,7 +568,7 @@ extern "C" int sd_logit_shape(hipStream_t stream, int R, int gamma_max, int V, i
   if (pen && (n_slots < 1 || ld_seen < words)) return SD_EINVAL;
   if (counts && (ld_counts < V || (ld_counts % 4) != 0 || (((uintptr_t)counts) & 15) != 0)) return SD_EINVAL;
   if (bias_off && (n_bias < 0 || (n_bias > 0 && (!bias_tok || !bias_val)))) return SD_EINVAL;
-  if (bias_off && n_bias > 0x7FFFFFFFLL) return SD_EUNSUPPORTED;
+  if (bias_off && n_bias > (1 << 30)) return SD_EUNSUPPORTED;
   if (mask && !mask_row0) return SD_EINVAL;
   if (mask_row0 && (n_mask_rows < 0 || (n_mask_rows > 0 && (!mask || ld_mask < words)))) return SD_EINVAL;
   ShapeArgs a;
@@ -659,7 +659,11 @@ extern "C" int sd_token_counts(hipStream_t stream, int R, int V, const int32_t* 
     const int most = mean < kOwnLongList ? kOwnMaxChunk / 2 : kOwnMaxChunk;
     a.chunk = V < most ? (V + 63) / 64 * 64 : most;
     const int n_ch = (V + a.chunk - 1) / a.chunk;
-    SDV_TRY_LAUNCH(sdv::launch(k_count_own, dim3(R, n_ch), dim3(kOwnThreads), a.chunk * sizeof(uint32_t), stream, a));
+    const size_t lds = a.chunk * sizeof(uint32_t);
+    if (lds > 64 * 1024)
+      SDV_TRY_LAUNCH(hipFuncSetAttribute((const void*)k_count_own, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)lds));
+    SDV_TRY_LAUNCH(sdv::launch(k_count_own, dim3(R, n_ch), dim3(kOwnThreads), lds, stream, a));
     return SD_OK;
   }
   if (reset)

@@ -500,13 +500,14 @@ extern "C" int sd_slot_reserve(hipStream_t stream, int R, int q_max, int block_s
   if ((long long)block_size * max_blocks > lim || (long long)R * q_max > lim || (long long)R * max_blocks > lim ||
       max_rows > lim)
     return SD_EUNSUPPORTED;
-  if (R == 0) return SD_OK;
-  if (padded ? max_rows < R * q_max : max_rows < 1) return SD_ERANGE;
-  if (!seq_len || !ell || !block_table || (n_blocks > 0 && !free_list) || !free_count || !ell_out || !row0 || !cu_rows ||
-      !ctx_len || !batch || !free_left || !row_req || !row_pos || !row_slot || !status)
+  if (padded ? max_rows < R * q_max : (R > 0 && max_rows < 1)) return SD_ERANGE;
+  if (!free_count || !cu_rows || !batch || !free_left) return SD_EINVAL;
+  if (max_rows > 0 && (!row_req || !row_pos || !row_slot)) return SD_EINVAL;
+  if (R > 0 && (!seq_len || !ell || !block_table || (n_blocks > 0 && !free_list) || !ell_out || !row0 || !ctx_len ||
+                !status))
     return SD_EINVAL;
-  if (row_token && !tokens && !(x0 && q_max == 1)) return SD_EINVAL;
-  if (row_token && ld_tokens < (x0 ? q_max - 1 : q_max)) return SD_ERANGE;
+  if (R > 0 && row_token && !tokens && !(x0 && q_max == 1)) return SD_EINVAL;
+  if (R > 0 && row_token && ld_tokens < (x0 ? q_max - 1 : q_max)) return SD_ERANGE;
   if (!workspace || workspace_bytes < sd_slot_reserve_workspace_size(R)) return SD_ERANGE;
   if (((uintptr_t)workspace & 7) != 0) return SD_EINVAL;
   ReserveArgs a;
@@ -541,8 +542,9 @@ extern "C" int sd_slot_reserve(hipStream_t stream, int R, int q_max, int block_s
   a.ld_tokens = ld_tokens;
   // a thread per row and, as far as the grid goes, a wave per request
   const int row_wgs = (max_rows + kFillThreads - 1) / kFillThreads, req_wgs = (R + 3) / 4;
-  const unsigned wgs = (unsigned)(row_wgs > req_wgs ? row_wgs : req_wgs);
-  const bool over = ell_out == ell || free_left == free_count;   // an output in an input's place
+  const unsigned wgs = (unsigned)(row_wgs > req_wgs ? row_wgs : (req_wgs > 1 ? req_wgs : 1));
+  // an output in an input's place (without requests only the count is read, and stays)
+  const bool over = R > 0 && (ell_out == ell || free_left == free_count);
   if (R <= kOneLaunchRequests && (!over || wgs == 1)) {
     const auto k = R <= kFillThreads ? k_reserve_all<1> : (R <= 2 * kFillThreads ? k_reserve_all<2> : k_reserve_all<4>);
     SDV_TRY_LAUNCH(sdv::launch(k, dim3(wgs < kOneLaunchGrid ? wgs : kOneLaunchGrid), dim3(kFillThreads), 0, stream, a));
@@ -570,11 +572,11 @@ extern "C" int sd_slot_commit(hipStream_t stream, int R, int q_max, int block_si
   if ((long long)block_size * max_blocks > lim || (long long)R * max_blocks + n_blocks > lim ||
       (long long)R * q_max > lim)
     return SD_EUNSUPPORTED;
-  if (R == 0) return SD_OK;
-  if (!seq_len || !ell || !n_accepted || !block_table || (n_blocks > 0 && !free_list) || !free_count ||
-      !seq_len_out || !n_new || !free_count_out)
+  if (!free_count || !free_count_out) return SD_EINVAL;
+  if (R > 0 && (!seq_len || !ell || !n_accepted || !block_table || (n_blocks > 0 && !free_list) || !seq_len_out ||
+                !n_new))
     return SD_EINVAL;
-  if (x0_out && (!out_tokens || !x0)) return SD_EINVAL;
+  if (R > 0 && x0_out && (!out_tokens || !x0)) return SD_EINVAL;
   if (!workspace || workspace_bytes < sd_slot_commit_workspace_size(R)) return SD_ERANGE;
   if (((uintptr_t)workspace & 7) != 0) return SD_EINVAL;
   CommitArgs a;
@@ -599,7 +601,7 @@ extern "C" int sd_slot_commit(hipStream_t stream, int R, int q_max, int block_si
   a.bs = block_size;
   a.max_blocks = max_blocks;
   a.n_blocks = n_blocks;
-  const unsigned wgs = (unsigned)((R + kCommitRequests - 1) / kCommitRequests);
+  const unsigned wgs = R > 0 ? (unsigned)((R + kCommitRequests - 1) / kCommitRequests) : 1;
   const bool over = seq_len_out == seq_len || free_count_out == free_count || (x0_out && x0_out == x0);
   if (R <= kOneLaunchRequests && (!over || wgs == 1)) {
     const auto k = R <= kFillThreads ? k_commit_all<1> : (R <= 2 * kFillThreads ? k_commit_all<2> : k_commit_all<4>);

@@ -435,10 +435,11 @@ int sd_uniforms(hipStream_t stream, uint64_t seed, long long n, const int64_t* r
  * A token that no term touches keeps its value.
  *
  *   R, gamma_max, V, ld, dtype as sd_verify; ell < 0: the request has no rows
- *   logits, out  [n_rows][ld], 16-byte aligned; out may be logits (only the
- *                touched parts of a row are then read and written), else the
- *                two do not overlap and rows outside the batch and entries
- *                past V are left as they are in out
+ *   logits, out  [n_rows][ld], 16-byte aligned; the rows of different
+ *                requests do not overlap; out may be logits (only the touched
+ *                parts of a row are then read and written), else the two do
+ *                not overlap and rows outside the batch and entries past V
+ *                are left as they are in out
  *   draft_tokens [R][gamma_max] int32, or NULL: no draft counts as written
  *   repetition (finite, > 0), frequency, presence (finite)  [R] fp32, each
  *                NULL for 1, 0 and 0
@@ -449,7 +450,8 @@ int sd_uniforms(hipStream_t stream, uint64_t seed, long long n, const int64_t* r
  *                presence
  *   slot         [R] int32 state row of each request, or NULL: r
  *   bias_off     [R + 1] int64 or NULL: request r's entries are
- *                bias_off[r]..bias_off[r+1]-1 of bias_tok, bias_val [n_bias]
+ *                bias_off[r]..bias_off[r+1]-1 of bias_tok, bias_val [n_bias],
+ *                n_bias <= 2^30
  *   mask         [n_mask_rows][ld_mask] 32-bit words in seen's layout, or
  *                NULL; row i of request r uses row mask_row0[r] + i, and a
  *                request with mask_row0[r] < 0 has no mask
@@ -529,8 +531,10 @@ int sd_token_counts(hipStream_t stream, int R, int V, const int32_t* tokens, lon
  *              BAD_INPUT where seq_len is negative or past the table (no
  *              rows, ctx_len 0) or a block id is outside [0, n_blocks) (its
  *              rows have slot -1)
- * ell_out may be ell and free_left may be free_count; seq_len is not changed,
- * so a step that is not committed is repeated by passing the old free_count.
+ * ell_out may be ell and free_left may be free_count (for more than one
+ * workgroup's rows this takes two launches); seq_len is not changed, so a
+ * step that is not committed is repeated by passing the old free_count.
+ * R = 0 writes the totals and the rows alone.
  *
  * sd_slot_commit - after verification: n_new[r] = 1 + min(n_accepted[r],
  * ell[r]) tokens of the step stay (0 where ell[r] < 0 or status[r] has
@@ -548,8 +552,9 @@ int sd_token_counts(hipStream_t stream, int R, int V, const int32_t* tokens, lon
  *   seq_len_out [R] int64 (usable as pos0 of the random decisions), n_new
  *   [R] int32, free_count_out [1]; x0_out [R] int32 or NULL: the next anchors
  *   out_tokens[r][n_accepted[r]] (x0[r] where n_new is 0).  seq_len_out,
- *   x0_out and free_count_out may be seq_len, x0 and free_count.  The entries
- *   of block_table stay as they are.
+ *   x0_out and free_count_out may be seq_len, x0 and free_count (from five
+ *   requests on this takes two launches).  The entries of block_table stay as
+ *   they are.  R = 0 writes free_count_out alone.
  *
  * block_size * max_blocks, R * q_max, R * max_blocks (sd_slot_commit: +
  * n_blocks) and max_rows are at most 2^31 - 257; workspaces of sd_slot_*_workspace_size(R) bytes.

@@ -400,6 +400,22 @@ def test_counts_skip_tokens_outside_and_requests_out_of_range():
     assert int(seen[0, 0]) == 6 and int(seen.sum()) == 6
 
 
+def test_nothing_to_do():
+    i = lambda *k: torch.zeros(k, dtype=torch.int32, device=DEV)  # noqa: E731
+    x = torch.ones((3, 64), device=DEV)
+    assert sdv.sd_logit_shape(x, i(0), i(0), 64, gamma_max=2)["status"].numel() == 0
+    got = sdv.sd_logit_shape(x, i(2), i(2), 64, gamma_max=0, mask=i(0, 2), mask_row0=i(2) - 1,
+                             bias=(i(3).long(), i(0), torch.zeros(0, device=DEV)), out=dict(logits=x * 0))
+    assert torch.equal(got["logits"][0], x[0]) and (got["status"] == 0).all()
+    got = sdv.sd_logit_shape(x, i(1), i(1), 64, gamma_max=0, mask=i(0, 2), mask_row0=i(1))
+    assert int(got["status"]) == sdv.SD_ST_BAD_INPUT      # a mask row that is not there
+    assert sdv.sd_token_counts(i(0, 4), i(1, 2), None, 64)["status"].numel() == 0
+    seen = i(2, 2) + 3
+    for reset, want in ((None, 3), (i(2) + 1, 0)):
+        assert (sdv.sd_token_counts(i(2, 0), seen, None, 64, reset=reset)["status"] == 0).all()
+        assert (seen == want).all()
+
+
 def test_counts_then_shape_equals_drafts_as_written():
     """Tokens entered into the state do to a row what the same tokens do as
     drafts before it."""

@@ -153,6 +153,21 @@ def test_commit_extremes():
         _commit(seq, ell, acc, table, free, f, bs, q, status=status)
 
 
+@pytest.mark.parametrize("rows", [0, 1, 700])
+def test_a_step_without_requests(rows):
+    i = lambda *k: torch.full(k, 9, dtype=torch.int32, device=DEV)  # noqa: E731
+    seq = torch.zeros(0, dtype=torch.int64, device=DEV)
+    for F, n in ((5, 5), (12, 8), (-2, 0)):
+        for padded in (False, True):
+            o = sdv.sd_slot_reserve(seq, i(0), i(0, 4), i(8), i(1) * 0 + F, 16, 3, max_rows=rows, padded=padded)
+            assert int(o["batch"]) == 0 and int(o["free_count"]) == n and o["cu_rows"].tolist() == [0]
+            assert all((o[k] == -1).all() and o[k].numel() == rows for k in ("row_req", "row_pos", "row_slot"))
+        c = i(1) * 0 + F
+        sdv.sd_slot_reserve(seq, i(0), i(0, 4), i(8), c, 16, 3, max_rows=rows, out=dict(free_count=c))
+        assert int(c) == n
+        assert int(sdv.sd_slot_commit(seq, i(0), i(0), i(0, 4), i(8), i(1) * 0 + F, 16, q_max=3)["free_count"]) == n
+
+
 def test_a_step_is_repeated_with_the_old_count():
     g = np.random.default_rng(6)
     seq, ell = np.array([3, 9, 0]), np.array([4, 4, 4])

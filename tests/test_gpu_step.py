@@ -115,7 +115,8 @@ def test_loop_against_the_oracle():
                                         float(freq[r]), float(pres[r]), (), mask[m0[r] + i] if m0[r] >= 0 else None)
                 fin = np.isfinite(row)
                 assert np.array_equal(fin, np.isfinite(rows[e]))
-                assert (np.abs(rows[e] - row)[fin] <= 2.0 ** -23 * mag[fin]).all(), (step, r, i)
+                # half a step of each intermediate and of the result, itself the last of them
+                assert (np.abs(rows[e][fin] - row[fin]) <= 2.0 ** -23 * mag[fin]).all(), (step, r, i)
                 shaped[e] = rows[e]   # verified as they are
         ora = OV.verify(shaped, want["row0"], n(L.drf).astype(np.float64), n(L.drf_row0), d,
                         np.maximum(want["ell"], 0), V, 1.0, 77, seq)
