@@ -451,7 +451,9 @@ int sd_uniforms(hipStream_t stream, uint64_t seed, long long n, const int64_t* r
  *   slot         [R] int32 state row of each request, or NULL: r
  *   bias_off     [R + 1] int64 or NULL: request r's entries are
  *                bias_off[r]..bias_off[r+1]-1 of bias_tok, bias_val [n_bias],
- *                n_bias <= 2^30
+ *                n_bias <= 2^30.  Lists are meant to be short (every 512
+ *                tokens of a row's width read the request's list); what bars
+ *                much of the vocabulary belongs into a mask
  *   mask         [n_mask_rows][ld_mask] 32-bit words in seen's layout, or
  *                NULL; row i of request r uses row mask_row0[r] + i, and a
  *                request with mask_row0[r] < 0 has no mask
