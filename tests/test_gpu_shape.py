@@ -400,6 +400,36 @@ def test_counts_skip_tokens_outside_and_requests_out_of_range():
     assert int(seen[0, 0]) == 6 and int(seen.sum()) == 6
 
 
+def test_state_and_lists_past_32_bit_offsets():
+    """State rows past 2^32 elements and lists past 2^31 tokens."""
+    V, S = 151936, 28400
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=DEV)  # noqa: E731
+    seen = torch.empty((S, V // 32), dtype=torch.int32, device=DEV)
+    counts = torch.empty((S, V), dtype=torch.int32, device=DEV)
+    s = S - 2
+    assert s * V > 1 << 32
+    for t in (seen, counts):
+        t[s - 1:] = 7
+    at = (1 << 31) + 5
+    toks = torch.empty(at + 20, dtype=torch.int32, device=DEV)
+    toks[at:] = torch.arange(20, dtype=torch.int32, device=DEV) * 7000 + 11
+    start = torch.tensor([at], device=DEV)
+    for reset in (i32(1), None):     # through LDS, then through LDS and by atomics onto what is there
+        sdv.sd_token_counts(toks, seen, counts, V, start=start, length=i32(20), slot=i32(s), reset=reset)
+    sdv.sd_token_counts(toks[at:at + 20].view(1, 20), seen, counts, V, slot=i32(s))
+    want = torch.zeros(V, dtype=torch.int32, device=DEV)
+    want[toks[at:].long()] = 3
+    assert torch.equal(counts[s], want)
+    assert torch.equal(seen[s], torch.as_tensor(OS.pack_bits(to_np(want)[None] > 0)).to(DEV)[0])
+    for t in (seen, counts):
+        assert (t[s - 1] == 7).all() and (t[s + 1] == 7).all()
+    x = torch.ones((1, V), device=DEV)
+    f = lambda v: torch.full((1,), v, device=DEV)  # noqa: E731
+    got = sdv.sd_logit_shape(x, i32(0), i32(0), V, gamma_max=0, repetition=f(2.0), frequency=f(0.25), seen=seen,
+                             counts=counts, slot=i32(s))["logits"][0]
+    assert torch.equal(got, torch.where(want > 0, 0.5 - 0.75, 1.0))
+
+
 def test_nothing_to_do():
     i = lambda *k: torch.zeros(k, dtype=torch.int32, device=DEV)  # noqa: E731
     x = torch.ones((3, 64), device=DEV)

@@ -153,6 +153,17 @@ def test_commit_extremes():
         _commit(seq, ell, acc, table, free, f, bs, q, status=status)
 
 
+def test_slots_past_32_bits():
+    """Block ids times the block size past 2^32."""
+    bs, pool = 256, 1 << 25
+    free = np.full(pool, -1, np.int32)
+    free[:6] = pool - 1 - np.arange(6)
+    table = np.full((2, 4), pool - 9, np.int32)
+    seq, ell = np.array([5, 300]), np.array([600, 3])
+    want, _ = _reserve(seq, ell, table, free, 6, bs, 700, 700, False)
+    assert want["row_slot"].max() > 1 << 32 and (want["status"] == 0).all()
+
+
 @pytest.mark.parametrize("rows", [0, 1, 700])
 def test_a_step_without_requests(rows):
     i = lambda *k: torch.full(k, 9, dtype=torch.int32, device=DEV)  # noqa: E731

@@ -26,15 +26,15 @@ class Loop:
     """R requests, all state on the device; `logits` stands for the target:
     rows of a step are a fixed table's rows by (token, position)."""
 
-    def __init__(self, seed=0):
+    def __init__(self, seed=0, pool=R * MB - 20):
         g = torch.Generator(device=DEV).manual_seed(seed)
         rand = lambda *k: torch.rand(k, generator=g, device=DEV)  # noqa: E731
         i32 = lambda *k: torch.zeros(k, dtype=torch.int32, device=DEV)  # noqa: E731
         ints = lambda hi, *k: torch.randint(0, hi, k, generator=g, device=DEV, dtype=torch.int32)  # noqa: E731
         self.model = torch.randn((V, V), generator=g, device=DEV) * 2.0
         self.seq = torch.zeros(R, dtype=torch.int64, device=DEV)
-        self.table, self.F = i32(R, MB) - 1, i32(1) + (R * MB - 20)
-        self.free = torch.randperm(R * MB - 20, generator=g, device=DEV).to(torch.int32)
+        self.table, self.F = i32(R, MB) - 1, i32(1) + pool
+        self.free = torch.randperm(pool, generator=g, device=DEV).to(torch.int32)
         self.x0, self.seen, self.counts = ints(V, R), i32(R, WORDS), i32(R, V)
         self.rep, self.freq, self.pres = 1.0 + rand(R), 0.5 * rand(R), 0.5 * rand(R)
         self.mask = torch.where(rand(R * Q, V) < 0.7, 1, 0)
@@ -87,15 +87,17 @@ class Loop:
             getattr(self, k).copy_(s[k])
 
 
-def test_loop_against_the_oracle():
-    L = Loop()
+@pytest.mark.parametrize("pool", [R * MB - 20, 14])
+def test_loop_against_the_oracle(pool):
+    """With few blocks requests go short, and some sit steps out."""
+    L = Loop(pool=pool)
     n = lambda t: to_np(t).copy()  # noqa: E731
     seen, counts = np.zeros((R, V), bool), np.zeros((R, V), int)
     model, drafts, mask = n(L.model).astype(np.float64), n(L.drafts), n(L.mask).astype(bool)
     m0, rep, freq, pres = n(L.m0), n(L.rep), n(L.freq), n(L.pres)
     table, free, F = n(L.table), n(L.free), int(L.F[0])
     seq, x0 = n(L.seq), n(L.x0)
-    released = 0
+    released, short, none = 0, 0, 0
     for step in range(25):
         L.release.copy_(torch.tensor([(step + r) % 9 == 8 for r in range(R)]).to(torch.int32))
         L.drafts.copy_(torch.as_tensor((drafts * (step + 1) + 7 * step) % V, dtype=torch.int32))
@@ -106,6 +108,8 @@ def test_loop_against_the_oracle():
         want = OL.reserve(seq, ell, table, free, F, BS, Q, R * Q, False, x0, d)
         for k, v in want.items():
             assert np.array_equal(n(L.buf["slots"][k]), v), (step, k)
+        short += int((want["status"] == OL.NO_SLOT).sum())
+        none += int((want["ell"] < 0).sum())
         rows = n(L.rows).astype(np.float64)
         shaped = rows.copy()
         for r in range(R):
@@ -135,6 +139,7 @@ def test_loop_against_the_oracle():
             OS.enter_tokens(seen[r], counts[r], got["tokens"][r][:c["n_new"][r]])
         assert np.array_equal(n(L.seen), OS.pack_bits(seen)) and np.array_equal(n(L.counts), counts)
     assert released and counts.sum() > 25
+    assert (short > 0) == (none > 0) == (pool == 14)
     blocks = sum((table[r, :-(-int(seq[r]) // BS)].tolist() for r in range(R)), []) + free[:F].tolist()
     assert sorted(blocks) == list(range(len(free)))
 
@@ -191,6 +196,78 @@ def test_loop_replays_from_a_graph():
         for w in b.ws.values():
             w.fill_(i)     # nothing is kept in a workspace from one step to the next
         torch.cuda.synchronize()
+        _same(a.state(), b.state())
+
+
+def test_parts_replay_from_a_graph():
+    """Lists entered through LDS, slots and their commit with outputs of their
+    own, captured once and replayed with eager work in between."""
+    g = torch.Generator(device=DEV).manual_seed(9)
+    ints = lambda hi, *k: torch.randint(0, hi, k, generator=g, device=DEV, dtype=torch.int32)  # noqa: E731
+    V1, n, r = 40000, 9000, 40
+    toks, seen, counts = ints(V1, 3, n), ints(9, 3, 1250), ints(9, 3, V1)
+    reset = torch.ones(3, dtype=torch.int32, device=DEV)
+    seq, ell = ints(50, r).long(), ints(9, r)
+    table, free = ints(500, r, 16), torch.randperm(500, generator=g, device=DEV).to(torch.int32)
+    F = torch.full((1,), 300, dtype=torch.int32, device=DEV)
+    e32 = lambda *k: torch.empty(k, dtype=torch.int32, device=DEV)  # noqa: E731
+    so = dict(ell=e32(r), row0=e32(r), cu_rows=e32(r + 1), ctx_len=e32(r), batch=e32(1), free_count=e32(1),
+              row_req=e32(300), row_pos=e32(300), row_slot=e32(300).long(), row_token=e32(300), status=e32(r))
+    co = dict(seq_len=e32(r).long(), x0=e32(r), n_new=e32(r), free_count=e32(1))
+    st = e32(3)
+    ws = torch.empty(1 << 16, dtype=torch.uint8, device=DEV)
+    x0, drafts, acc, rel = ints(99, r), ints(99, r, 9), ints(9, r), ints(2, r)
+
+    def call():
+        sdv.sd_token_counts(toks, seen, counts, V1, reset=reset, out=dict(status=st))
+        sdv.sd_slot_reserve(seq, ell, table, free, F, 8, 9, x0=x0, tokens=drafts, out=so, workspace=ws)
+        sdv.sd_slot_commit(seq, so["ell"], acc, table, free, so["free_count"], 8, out_tokens=drafts, x0=x0,
+                           release=rel, out=co, workspace=ws)
+
+    outs = {**so, **{"c_" + k: v for k, v in co.items()}, "st": st, "seen": seen, "counts": counts, "free": free,
+            "table": table}
+    before = {k: outs[k].clone() for k in ("free", "table")}   # a step changes them: each begins from here
+    call()
+    torch.cuda.synchronize()
+    ref = {k: v.clone() for k, v in outs.items()}
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            call()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    for i in range(3):
+        for k, v in outs.items():
+            if k in before:
+                v.copy_(before[k])
+            else:
+                v.fill_(-3)
+        ws.fill_(i)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for k, v in ref.items():
+            assert torch.equal(outs[k], v), (i, k)
+
+
+def test_two_loops_at_once():
+    """Two loops on two streams, nothing shared, give what each gives alone."""
+    alone, both = [Loop(11), Loop(12)], [Loop(11), Loop(12)]
+    for L in alone:
+        for _ in range(5):
+            L.step()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in both]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for L, s in zip(both, streams):
+            with torch.cuda.stream(s):
+                L.step()
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
         _same(a.state(), b.state())
 
 
