@@ -16,11 +16,12 @@ namespace {
 constexpr int kShapeThreads = 64;
 constexpr int kVecTokens = 8;                              // tokens per thread: one mask byte
 constexpr int kShapeChunk = kShapeThreads * kVecTokens;    // tokens per workgroup
-// Resident waves of the chip at this kernel's registers: a batch with fewer
-// (request, chunk) waves splits its rows over more (64 requests, V = 32000:
-// 14.9 us split in two, 20.8 us unsplit; 4 requests, V = 1000: 4.0 and 8.5 us;
-// a batch that fills the chip anyway loses 100 us of 460 by a split in two).
-constexpr long long kFullWaves = 8192;
+// A batch with fewer (request, chunk) waves, two rounds of what the chip holds
+// at this kernel's registers, splits its rows over more (64 requests, V =
+// 32000: 15 us split in two, 21 us unsplit; 4 requests, V = 1000: 4.0 and 8.5
+// us; 16 requests with 9 rows, V = 151936: 20.3 us, 23.6 us with one round; a
+// batch that fills the chip anyway loses 100 us of 460 by a split in two).
+constexpr long long kFullWaves = 16384;
 // Beyond this the rows do not stay in the 256 MB last-level cache: they are
 // streamed past it and wait for their masks (512 requests, V = 151936: 461 us
 // streamed, 548 us not; 64 requests, V = 32000: 17.1 and 15.9 us).
@@ -69,7 +70,7 @@ struct Oct<true> {
   SDV_DEV uint32_t& word(int k) { return k == 0 ? q.x : (k == 1 ? q.y : (k == 2 ? q.z : q.w)); }
   SDV_DEV float get(int e) { return e & 1 ? sdv::bf16hi(word(e >> 1)) : sdv::bf16lo(word(e >> 1)); }
   SDV_DEV void set(int e, float x) {
-    const uint32_t h = sdv::f32_to_bf16_rne(x);
+    const uint32_t h = __builtin_bit_cast(uint16_t, (__bf16)x);   // nearest-even in one instruction
     uint32_t& w = word(e >> 1);
     w = e & 1 ? (w & 0xFFFFu) | (h << 16) : (w & 0xFFFF0000u) | h;
   }
@@ -121,6 +122,7 @@ struct Request {
   int row0, srow, m0;
   int64_t b0, b1;
   float rep, freq, pres;
+  float inv;   // 1 / rep
   bool pen, ok;
 };
 SDV_DEV Request read_request(const ShapeArgs& a, int r) {
@@ -135,6 +137,7 @@ SDV_DEV Request read_request(const ShapeArgs& a, int r) {
   q.b0 = a.bias_off ? a.bias_off[r] : 0;
   q.b1 = a.bias_off ? a.bias_off[r + 1] : 0;
   const float inf = __builtin_huge_valf();
+  q.inv = 1.0f / q.rep;
   q.pen = q.rep != 1.0f || q.freq != 0.0f || q.pres != 0.0f;
   q.ok = q.row0 >= 0 && (int64_t)q.row0 + q.n <= a.n_rows;
   q.ok = q.ok && q.rep > 0.0f && q.rep < inf && fabsf(q.freq) < inf && fabsf(q.pres) < inf;
@@ -142,6 +145,18 @@ SDV_DEV Request read_request(const ShapeArgs& a, int r) {
   q.ok = q.ok && (q.m0 < 0 || (int64_t)q.m0 + q.n <= a.n_mask_rows);
   q.ok = q.ok && q.b0 >= 0 && q.b0 <= q.b1 && q.b1 <= a.n_bias;
   return q;
+}
+
+// y / rep where y > 0, else y * rep.  The quotient is y * inv and one step of
+// correction, u + inv * (y - u * rep): u is within 1.5 units, so the corrected
+// sum is within 2^-23 of a unit before its rounding (waves with many seen
+// tokens are bound by instructions: the divide's own sequence took 14.4 us
+// where this takes 13.8, for 64 requests at V = 32000).  An overflowing u (y
+// or 1 / rep out of range) is divided.
+SDV_DEV float penalised(const Request& q, float y) {
+  float u = y * (y > 0.0f ? q.inv : q.rep);
+  if (y > 0.0f) u = u < __builtin_huge_valf() ? fmaf(fmaf(-u, q.rep, y), q.inv, u) : y / q.rep;
+  return u;
 }
 
 // What a lane holds for its eight tokens v0..v0+7.
@@ -175,9 +190,8 @@ struct Tokens {
       if ((hit >> e) & 1) {
         float y = x.get(e);
         if ((met >> e) & 1) {
-          y = y > 0.0f ? y / q.rep : y * q.rep;
-          y -= q.freq * c[e];
-          if (c[e] > 0.0f) y -= q.pres;
+          y = penalised(q, y);
+          y = fmaf(-q.freq, c[e], y) - (c[e] > 0.0f ? q.pres : 0.0f);
         }
         if ((biased >> e) & 1) y += bias[e];
         x.set(e, y);
