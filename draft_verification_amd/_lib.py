@@ -467,13 +467,16 @@ def _on_device(fn):
     return wrapper
 
 
+_Tensor = torch.Tensor
+
+
 def _arg(t, dtype, name, index, n=None):
     """The address of tensor t (None: NULL) after checking its type, that it
     is contiguous and on device `index`, and its number of elements where
     given."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype is dtype and t.get_device() == index and t.is_contiguous() and (n is None or t.numel() == n):
         return t.data_ptr()
@@ -536,8 +539,8 @@ def sd_logit_shape(logits, row0, ell, V, gamma_max=None, draft_tokens=None, repe
     if mask is not None and mask.dim() != 2:
         raise ValueError("mask must be 2-D")
     o = out or {}
-    dst = _out(o, "logits", lambda: torch.empty_like(logits))
-    status = _out(o, "status", lambda: torch.empty(R, dtype=torch.int32, device=logits.device))
+    dst = o["logits"] if "logits" in o else torch.empty_like(logits)
+    status = o["status"] if "status" in o else torch.empty(R, dtype=torch.int32, device=logits.device)
     if dst.shape != logits.shape:
         raise ValueError(f"out must have the logits' shape {list(logits.shape)}, got {list(dst.shape)}")
     i32, f32, ldt = torch.int32, torch.float32, logits.dtype
@@ -578,7 +581,7 @@ def sd_token_counts(tokens, seen, counts, V, start=None, length=None, prompt_len
     if seen is None:
         raise ValueError("seen is needed")
     n_slots, ld_seen, ld_counts = _state_rows(seen, counts, V)
-    status = _out(out or {}, "status", lambda: torch.empty(R, dtype=torch.int32, device=tokens.device))
+    status = out["status"] if out and "status" in out else torch.empty(R, dtype=torch.int32, device=tokens.device)
     i32 = torch.int32
     code = lib().sd_token_counts(
         _raw_stream(dev), R, int(V), _arg(tokens, i32, "tokens", dev), tokens.numel(), width,
@@ -615,13 +618,12 @@ def sd_slot_reserve(seq_len, ell, block_table, free_list, free_count, block_size
     if max_rows is None:
         max_rows = o["row_req"].numel() if "row_req" in o else R * q_max
     i64 = torch.int64
-    make = lambda k, dt=i32: torch.empty(k, dtype=dt, device=device)  # noqa: E731
-    with_tokens = x0 is not None or tokens is not None
-    res = {k: o[k] if k in o else make(size)
-           for k, size in (("ell", R), ("row0", R), ("cu_rows", R + 1), ("ctx_len", R), ("batch", 1),
-                           ("free_count", 1), ("row_req", max_rows), ("row_pos", max_rows), ("status", R))}
-    res["row_slot"] = o["row_slot"] if "row_slot" in o else make(max_rows, i64)
-    res["row_token"] = None if not with_tokens else o["row_token"] if "row_token" in o else make(max_rows)
+    make = lambda k, n, dt=i32: o[k] if k in o else torch.empty(n, dtype=dt, device=device)  # noqa: E731
+    res = dict(ell=make("ell", R), row0=make("row0", R), cu_rows=make("cu_rows", R + 1), ctx_len=make("ctx_len", R),
+               batch=make("batch", 1), free_count=make("free_count", 1), row_req=make("row_req", max_rows),
+               row_pos=make("row_pos", max_rows), row_slot=make("row_slot", max_rows, i64),
+               row_token=None if x0 is None and tokens is None else make("row_token", max_rows),
+               status=make("status", R))
     ws = workspace if workspace is not None else _workspace(sd_slot_reserve_workspace_size(R), device)
     code = lib().sd_slot_reserve(
         _raw_stream(dev), R, int(q_max), int(block_size), mb, free_list.numel(), max_rows, 1 if padded else 0,
@@ -669,11 +671,9 @@ def sd_slot_commit(seq_len, ell, n_acc, block_table, free_list, free_count, bloc
     o = out or {}
     i32 = torch.int32
     i64 = torch.int64
-    make = lambda k, dt=i32: torch.empty(k, dtype=dt, device=device)  # noqa: E731
-    res = dict(seq_len=o["seq_len"] if "seq_len" in o else make(R, i64),
-               n_new=o["n_new"] if "n_new" in o else make(R),
-               free_count=o["free_count"] if "free_count" in o else make(1),
-               x0=None if out_tokens is None else o["x0"] if "x0" in o else make(R))
+    make = lambda k, n, dt=i32: o[k] if k in o else torch.empty(n, dtype=dt, device=device)  # noqa: E731
+    res = dict(seq_len=make("seq_len", R, i64), n_new=make("n_new", R), free_count=make("free_count", 1),
+               x0=None if out_tokens is None else make("x0", R))
     ws = workspace if workspace is not None else _workspace(sd_slot_commit_workspace_size(R), device)
     code = lib().sd_slot_commit(
         _raw_stream(dev), R, int(q_max), int(block_size), mb, free_list.numel(),

@@ -417,19 +417,21 @@ __global__ __launch_bounds__(kCountThreads) void k_count_clear(CountArgs a) {
 // coalesced (without a reset: adds to what the lists touch).  A word of LDS
 // holds a token's count and, in its top bit, that it was seen.  Every range
 // reads the whole list; long lists are bound by the instructions of that
-// filter (and wait for the ranges of the frequent tokens), short ones by the
-// writing.  Measured at V = 151936: 96 lists of up to 131072 tokens 33 us
-// (252 us with a clearing pass and atomics on the state, 1.8 ms where half of
-// a list is one token); 256 lists of at most 100 tokens 33 us, 4.9 TB/s.
+// filter (and wait for the ranges of the longest), short ones by the writing.
+// Measured at V = 151936: 96 lists of up to 131072 tokens 26 us (252 us with a
+// clearing pass and atomics on the state, 1.8 ms where half of a list is one
+// token, here 34 us); one list of 131072 tokens 14.6 us; 256 lists of at most
+// 100 tokens 32 us, 5.0 TB/s.
 constexpr int kOwnThreads = 1024;
-constexpr int kOwnLoads = 8;             // 4: 39 us, 16: 34 us for the 96 lists
+constexpr int kOwnLoads = 16;            // 4: 30 us, 8: 27 us for the 96 lists
 constexpr int kOwnMaxChunk = 32768;      // 128 KB of the 160 KB of LDS
 // Lists below this mean length are entered in half as large ranges, two
-// workgroups per CU (256 short lists: 33 against 37 us; the 96 long ones
-// above: 36.5 against 34.5 us).
+// workgroups per CU (256 short lists: 32 against 39 us; the 96 long ones
+// above: 28 against 27 us).
 constexpr int kOwnLongList = 8192;
-// Without a reset, from this mean length on (64 lists of 2048 tokens: atomics
-// 12.7 us, ranges 15.0 us; of 8192 tokens: 48 and 23 us).
+// Without a reset, from this mean length on (64 lists of 4096 tokens: atomics
+// 24 us, ranges 16 us; of 512 tokens: 4.7 and 11 us; one list of 131072: 272
+// and 16.6 us).
 constexpr int kOwnMinList = 4096;
 // The search for shared state rows grows with the square of the requests
 // (8192 requests at V = 4000: 71 us, 38 us cleared first and added to).
@@ -437,36 +439,41 @@ constexpr int kOwnMaxRequests = 4096;
 constexpr uint32_t kSeenBit = 0x80000000u;
 
 // Enter n tokens into the workgroup's range: MARK sets the seen bit, else the
-// count grows.
+// count grows.  `spare` are 64 more words for the tokens of other ranges, one
+// per lane, so that the common path has no branch.
 template <bool MARK>
-SDV_DEV void enter_tokens(uint32_t* cell, const int32_t* tokens, int n, int v0, int width) {
-  const int tid = threadIdx.x;
+SDV_DEV void enter_tokens(uint32_t* cell, uint32_t* spare, const int32_t* tokens, int n, int v0, int width) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  auto add = [&](uint32_t* at, uint32_t k) {
+    if (MARK) atomicOr(at, kSeenBit);
+    else atomicAdd(at, k);
+  };
   auto one = [&](int tok) {
     const unsigned t = (unsigned)tok - (unsigned)v0;   // a negative token is past every range
-    if (t >= (unsigned)width) return;
-    // a stretch of one token would queue the wave's lanes at one word
-    const unsigned t0 = __builtin_amdgcn_readfirstlane(t);
-    const uint64_t lanes = __ballot(true);
-    if (__ballot(t == t0) == lanes) {
-      if ((tid & 63) == __builtin_ctzll(lanes)) {
-        if (MARK) atomicOr(&cell[t0], kSeenBit);
-        else atomicAdd(&cell[t0], (uint32_t)__popcll(lanes));
-      }
-    } else if (MARK) {
-      atomicOr(&cell[t], kSeenBit);
-    } else {
-      atomicAdd(&cell[t], 1u);
-    }
+    add(t < (unsigned)width ? cell + t : spare + lane, 1u);
   };
-  // the tokens of a round are requested together: a list is one chain of
-  // loads otherwise
+  // a wave takes kOwnLoads * 64 tokens in a row at a time, requested together:
+  // a list is one chain of loads otherwise
+  const int wave0 = (tid >> 6) * (kOwnLoads * 64) + lane;
   const int full = n - n % (kOwnLoads * kOwnThreads);
   for (int i = 0; i < full; i += kOwnLoads * kOwnThreads) {
     int tok[kOwnLoads];
 #pragma unroll
-    for (int k = 0; k < kOwnLoads; ++k) tok[k] = tokens[i + k * kOwnThreads + tid];
+    for (int k = 0; k < kOwnLoads; ++k) tok[k] = tokens[i + wave0 + k * 64];
+    // a stretch of one token would queue the wave's lanes at one word
+    const int tok0 = __builtin_amdgcn_readfirstlane(tok[0]);
+    if (__ballot(tok[0] == tok0) == ~0ull) {
 #pragma unroll
-    for (int k = 0; k < kOwnLoads; ++k) one(tok[k]);
+      for (int k = 0; k < kOwnLoads; ++k) {
+        const unsigned t0 = (unsigned)tok0 - (unsigned)v0;
+        const uint64_t with = __ballot(tok[k] == tok0);
+        if (tok[k] != tok0) one(tok[k]);
+        else if (t0 < (unsigned)width && lane == __builtin_ctzll(with)) add(cell + t0, (uint32_t)__popcll(with));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kOwnLoads; ++k) one(tok[k]);
+    }
   }
   for (int64_t i = full + tid; i < n; i += 4 * kOwnThreads) {
     int tok[4];
@@ -510,8 +517,8 @@ __global__ __launch_bounds__(kOwnThreads) void k_count_own(CountArgs a) {
   // a prompt's tokens are marked, the others counted
   auto enter = [&](int64_t from, int len, int prompt) {
     const int cut = a.counts ? sdv::clampi(prompt, 0, len) : len;
-    enter_tokens<true>(cell, a.tokens + from, cut, v0, width);
-    enter_tokens<false>(cell, a.tokens + from + cut, len - cut, v0, width);
+    enter_tokens<true>(cell, cell + a.chunk, a.tokens + from, cut, v0, width);
+    enter_tokens<false>(cell, cell + a.chunk, a.tokens + from + cut, len - cut, v0, width);
   };
   enter(at, n, a.prompt_len ? a.prompt_len[r] : 0);
   if (shared_row & 1)
@@ -673,7 +680,7 @@ extern "C" int sd_token_counts(hipStream_t stream, int R, int V, const int32_t* 
     const int most = mean < kOwnLongList ? kOwnMaxChunk / 2 : kOwnMaxChunk;
     a.chunk = V < most ? (V + 63) / 64 * 64 : most;
     const int n_ch = (V + a.chunk - 1) / a.chunk;
-    const size_t lds = a.chunk * sizeof(uint32_t);
+    const size_t lds = (a.chunk + 64) * sizeof(uint32_t);
     if (lds > 64 * 1024)
       SDV_TRY_LAUNCH(hipFuncSetAttribute((const void*)k_count_own, hipFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)lds));
