@@ -561,22 +561,25 @@ def sd_logit_shape(logits, row0, ell, V, gamma_max=None, draft_tokens=None, repe
 
 @_on_device
 def sd_token_counts(tokens, seen, counts, V, start=None, length=None, prompt_len=None, slot=None, reset=None,
-                    out=None, *, stream=None):
+                    out=None, max_length=0, *, stream=None):
     """Enter token lists into the state behind the penalties, in place: seen
     [n_slots][words] int32 (bits), counts [n_slots][ld] int32 or None.
     tokens: [R][width] int32 (entries outside [0, V) are skipped, such as the
-    -1 behind sd_verify's tokens), with length [R] int32 or None; or 1-D with
-    start [R] int64 and length.  prompt_len [R] int32: how many leading tokens
+    -1 behind sd_verify's tokens), with length [R] int32 or None; or any shape
+    with start [R] int64 (into all of it) and length, of at most max_length
+    where that is given: do so for short lists in a large buffer.  prompt_len [R] int32: how many leading tokens
     of each list are prompt; reset [R] int32: clear the state row first.
     Returns a dict: status."""
     dev = tokens.get_device()
     if start is not None:
-        R, width = start.numel(), 0
+        R, width = start.numel(), int(max_length)
         if length is None:
             raise ValueError("start needs length")
     else:
         if tokens.dim() != 2:
             raise ValueError("tokens must be [R][width] without start")
+        if max_length:
+            raise ValueError("max_length goes with start")
         R, width = tokens.shape
     if seen is None:
         raise ValueError("seen is needed")

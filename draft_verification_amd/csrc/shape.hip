@@ -373,6 +373,7 @@ SDV_DEV bool count_row(const CountArgs& a, int r, int64_t* at, int* n, int* srow
   *n = a.length ? a.length[r] : a.width;
   *srow = a.slot ? a.slot[r] : r;
   if (*n < 0) *n = 0;
+  if ((!a.start || a.width > 0) && *n > a.width) return false;   // a list ends with its row
   return *srow >= 0 && *srow < a.n_slots && *at >= 0 && *at <= a.n_tokens && *n <= a.n_tokens - *at;
 }
 
@@ -670,16 +671,19 @@ extern "C" int sd_token_counts(hipStream_t stream, int R, int V, const int32_t* 
   a.ld_seen = ld_seen;
   a.ld_counts = ld_counts;
   a.R = R;
+  // the lengths are on the device: what a list can hold on average
+  const long long room = start ? n_tokens / R : width;
+  const long long mean = start && width > 0 && width < room ? width : room;
   // workgroups per request: 2048 in all, as far as the work goes
   auto split = [&](long long work, long long each) {
     const long long fill = (2048 + R - 1) / R, need = (work + each - 1) / each;
     return (unsigned)(need < 1 ? 1 : (need < fill ? need : fill));
   };
-  const long long mean = (start ? n_tokens : (long long)R * width) / R;
-  if ((reset || mean >= kOwnMinList) && R <= kOwnMaxRequests) {
-    const int most = mean < kOwnLongList ? kOwnMaxChunk / 2 : kOwnMaxChunk;
-    a.chunk = V < most ? (V + 63) / 64 * 64 : most;
-    const int n_ch = (V + a.chunk - 1) / a.chunk;
+  const int most = mean < kOwnLongList ? kOwnMaxChunk / 2 : kOwnMaxChunk;
+  a.chunk = V < most ? (V + 63) / 64 * 64 : most;
+  const int n_ch = (V + a.chunk - 1) / a.chunk;
+  if ((reset || mean >= kOwnMinList) && R <= kOwnMaxRequests &&
+      (long long)R * n_ch * kOwnThreads <= 0xFFFFFFFFLL) {   // work-items of one launch
     const size_t lds = (a.chunk + 64) * sizeof(uint32_t);
     if (lds > 64 * 1024)
       SDV_TRY_LAUNCH(hipFuncSetAttribute((const void*)k_count_own, hipFuncAttributeMaxDynamicSharedMemorySize,
@@ -689,7 +693,7 @@ extern "C" int sd_token_counts(hipStream_t stream, int R, int V, const int32_t* 
   }
   if (reset)
     SDV_TRY_LAUNCH(sdv::launch(k_count_clear, dim3(R, split(V, kCountThreads)), dim3(kCountThreads), 0, stream, a));
-  SDV_TRY_LAUNCH(sdv::launch(k_count_add, dim3(R, split(start ? n_tokens : width, kCountThreads)),
+  SDV_TRY_LAUNCH(sdv::launch(k_count_add, dim3(R, split(width > 0 || !start ? width : n_tokens, kCountThreads)),
                              dim3(kCountThreads), 0, stream, a));
   return SD_OK;
 }

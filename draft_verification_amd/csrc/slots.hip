@@ -541,7 +541,7 @@ extern "C" int sd_slot_reserve(hipStream_t stream, int R, int q_max, int block_s
   a.padded = padded;
   a.ld_tokens = ld_tokens;
   // a thread per row and, as far as the grid goes, a wave per request
-  const int row_wgs = (max_rows + kFillThreads - 1) / kFillThreads, req_wgs = (R + 3) / 4;
+  const int row_wgs = (max_rows + kFillThreads - 1) / kFillThreads, req_wgs = R < 16384 ? (R + 3) / 4 : 4096;
   const unsigned wgs = (unsigned)(row_wgs > req_wgs ? row_wgs : (req_wgs > 1 ? req_wgs : 1));
   // an output in an input's place (without requests only the count is read, and stays)
   const bool over = R > 0 && (ell_out == ell || free_left == free_count);

@@ -478,9 +478,12 @@ int sd_logit_shape(hipStream_t stream, int R, int gamma_max, int V, int ld, int 
  * skipped), the bit of t in seen[slot[r]] is set, and for those past the
  * first prompt_len[r] counts[slot[r]][t] grows by one.
  *   tokens [n_tokens] int32; request r's list is tokens[start[r]] ..
- *   tokens[start[r] + length[r] - 1]; start NULL: r * width, length NULL
- *   (only without start): width; a negative length is 0.  sd_verify's
- *   out_tokens are a list of width gamma_max + 1.
+ *   tokens[start[r] + length[r] - 1]; start NULL: r * width, with lengths up
+ *   to width, length NULL (only without start): width; a negative length is
+ *   0.  With start, width > 0 bounds the lengths: give it where the lists
+ *   are short parts of a large buffer (the kernel is chosen by the length a
+ *   list can have, n_tokens / R where width is 0).  A longer list is out of
+ *   range.  sd_verify's out_tokens are lists of width gamma_max + 1.
  *   prompt_len [R] int32 or NULL (0): prompt tokens are seen, not counted
  *   reset      [R] int32 or NULL: where not 0 the state row is cleared first
  *              (whatever it held)

@@ -400,6 +400,49 @@ def test_counts_skip_tokens_outside_and_requests_out_of_range():
     assert int(seen[0, 0]) == 6 and int(seen.sum()) == 6
 
 
+@pytest.mark.parametrize("reset", [False, True])
+def test_counts_of_fixed_rows_with_lengths(reset):
+    """A length past its row is refused; others end a row early."""
+    i32 = lambda a: torch.as_tensor(a, dtype=torch.int32).to(DEV)  # noqa: E731
+    toks = i32([[1, 2, 3], [4, 5, 6], [7, 8, 9], [10, 11, 12]])
+    seen = torch.zeros((4, 2), dtype=torch.int32, device=DEV)
+    counts = torch.full((4, 64), 2, dtype=torch.int32, device=DEV)
+    got = sdv.sd_token_counts(toks, seen, counts, 64, length=i32([2, 4, 0, 3]),
+                              reset=i32([1, 1, 1, 0]) if reset else None)
+    assert to_np(got["status"]).tolist() == [0, sdv.SD_ST_BAD_INPUT, 0, 0]
+    want = np.full((4, 64), 2)
+    if reset:
+        want[0] = want[2] = 0
+    want[0, 1:3] += 1
+    want[3, 10:13] += 1
+    assert np.array_equal(to_np(counts), want)
+    assert to_np(seen)[:, 0].tolist() == [6, 0, 0, 7 << 10]
+
+
+def test_counts_of_short_lists_in_a_large_buffer():
+    """start into a [R][n] buffer, lengths bounded or not: the same counts."""
+    g = np.random.default_rng(12)
+    R, n, V = 5, 20000, 3000
+    toks = torch.as_tensor(g.integers(0, V, (R, n)), dtype=torch.int32).to(DEV)
+    length = g.integers(0, 8, R)
+    start = np.arange(R) * n + g.integers(0, n - 8, R)
+    want = np.zeros((R, V), int)
+    for r in range(R):
+        np.add.at(want[r], to_np(toks).ravel()[start[r]:start[r] + length[r]], 1)
+    for bound in (0, 7, 8):
+        seen = torch.zeros((R, (V + 31) // 32), dtype=torch.int32, device=DEV)
+        counts = torch.zeros((R, V), dtype=torch.int32, device=DEV)
+        got = sdv.sd_token_counts(toks, seen, counts, V, start=torch.as_tensor(start).to(DEV),
+                                  length=torch.as_tensor(length, dtype=torch.int32).to(DEV), max_length=bound)
+        assert (got["status"] == 0).all()
+        assert np.array_equal(to_np(counts), want) and np.array_equal(to_np(seen), OS.pack_bits(want > 0))
+    got = sdv.sd_token_counts(toks, seen, counts, V, start=torch.as_tensor(start).to(DEV), max_length=3,
+                              length=torch.as_tensor(length, dtype=torch.int32).to(DEV))
+    assert np.array_equal(to_np(got["status"]) != 0, length > 3)
+    with pytest.raises(ValueError, match="goes with start"):
+        sdv.sd_token_counts(toks, seen, counts, V, max_length=4)
+
+
 def test_state_and_lists_past_32_bit_offsets():
     """State rows past 2^32 elements and lists past 2^31 tokens."""
     V, S = 151936, 28400
