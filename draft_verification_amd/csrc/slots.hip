@@ -86,7 +86,7 @@ struct ReserveArgs {
   int32_t* row_token;
   int32_t* status;
   int32_t* ws_first;   // [R] index in the free list of the request's first new block, counting down
-  int32_t* ws_base;    // [R] tokens in the cache, or -1
+  int32_t* ws_base;    // [R] tokens in the cache
   int32_t* ws_cu;      // [R + 1]
   int R, q_max, bs, max_blocks, n_blocks, max_rows, padded, ld_tokens;
 };
