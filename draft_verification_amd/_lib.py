@@ -655,8 +655,10 @@ def sd_slot_commit(seq_len, ell, n_acc, block_table, free_list, free_count, bloc
                    *, stream=None):
     """Keep what verification accepted of a step and give the other blocks
     back.  seq_len [R] int64, ell [R] int32 and free_count [1] int32 as
-    sd_slot_reserve left them, n_acc, out_tokens [R][q_max], status sd_verify's,
-    x0 [R] int32 the step's anchors (with out_tokens: the next ones are
+    sd_slot_reserve left them, n_acc, out_tokens [R][q_max] sd_verify's,
+    status [R] int32 the statuses of the step's calls OR-ed (slots, shaping
+    and verification: a request that one of them refused keeps nothing of the
+    step), x0 [R] int32 the step's anchors (with out_tokens: the next ones are
     returned); release, keep [R] int32.  free_list is updated in place, and
     status where a request is refused.  Returns a dict of device tensors:
     seq_len, n_new, free_count, x0 (None without out_tokens)."""

@@ -362,6 +362,10 @@ struct CommitArgs {
   int R, q_max, bs, max_blocks, n_blocks;
 };
 
+// Statuses whose step is repeated: rows that could not be verified, or that a
+// call before verification left out.
+constexpr int kHeld = SD_ST_NONFINITE | SD_ST_ZERO_Z | SD_ST_BAD_INPUT;
+
 struct Committed {
   int64_t len;   // tokens that stay
   int n_new;
@@ -403,7 +407,7 @@ SDV_DEV void commit_scan(const CommitArgs& a, uint64_t* part, int* free_out, Emi
         c[k].bad = true;
       } else {
         c[k].acc = sdv::clampi(acc[k], 0, q ? L[k] : 0);
-        c[k].n_new = q && !(st[k] & (SD_ST_NONFINITE | SD_ST_ZERO_Z)) ? c[k].acc + 1 : 0;
+        c[k].n_new = q && !(st[k] & kHeld) ? c[k].acc + 1 : 0;
         const int held = blocks_of((int)len[k] + q, a.bs);
         c[k].len = done[k] ? 0 : len[k] + c[k].n_new;
         c[k].kept = done[k] ? sdv::clampi(keep[k], 0, held) : blocks_of((int)c[k].len, a.bs);
@@ -441,8 +445,14 @@ SDV_DEV void give_back(const CommitArgs& a, int r, int kept, int give, int to) {
 }
 
 // One launch: every workgroup repeats the scan and keeps the requests of its
-// waves.  No output may be an input unless the grid is one workgroup (the
-// status may: its new bit is not read).
+// waves.  No output may be an input unless the grid is one workgroup, but for
+// the status: a workgroup that already sees the bit that another one adds
+// (commit_out) comes to the same result.  A request out of range is so with
+// and without the bit.  One that gives back more than the pool holds (to +
+// give > n_blocks) would give back more yet if it were held; those after it
+// drop their blocks either way, for their `to` is past the pool in both, and
+// the count is the pool's.  Its own outputs come from the one workgroup that
+// writes its status, by the thread that has read it.
 template <int kItems>
 __global__ __launch_bounds__(kFillThreads) void k_commit_all(CommitArgs a) {
   __shared__ uint64_t part[kScanWaves];

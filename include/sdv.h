@@ -461,7 +461,8 @@ int sd_uniforms(hipStream_t stream, uint64_t seed, long long n, const int64_t* r
  *                penalties) a draft among x_1..x_ell, lies outside [0, V):
  *                it is skipped; BAD_INPUT where a row, slot, mask row, bias
  *                offset or penalty is out of range: none of the request's
- *                rows is written
+ *                rows is written, so what is drawn from them must not be kept
+ *                (see sd_slot_commit's status)
  */
 int sd_logit_shape(hipStream_t stream, int R, int gamma_max, int V, int ld, int dtype,
                    const void* logits, void* out, int n_rows, const int32_t* row0,
@@ -535,7 +536,7 @@ int sd_token_counts(hipStream_t stream, int R, int V, const int32_t* tokens, lon
  *   status     [R] int32: NO_SLOT where a request got fewer rows than asked;
  *              BAD_INPUT where seq_len is negative or past the table (no
  *              rows, ctx_len 0) or a block id is outside [0, n_blocks) (its
- *              rows have slot -1)
+ *              rows have slot -1; see sd_slot_commit's status)
  * ell_out may be ell and free_left may be free_count (for more than one
  * workgroup's rows this takes two launches); seq_len is not changed, so a
  * step that is not committed is repeated by passing the old free_count.
@@ -543,7 +544,8 @@ int sd_token_counts(hipStream_t stream, int R, int V, const int32_t* tokens, lon
  *
  * sd_slot_commit - after verification: n_new[r] = 1 + min(n_accepted[r],
  * ell[r]) tokens of the step stay (0 where ell[r] < 0 or status[r] has
- * NONFINITE or ZERO_Z: the step is repeated), seq_len grows by n_new, and the
+ * NONFINITE, ZERO_Z or BAD_INPUT: the step is repeated), seq_len grows by
+ * n_new, and the
  * blocks past the new length go back, request after request, to
  * free_list[free_count..].  Where release[r] is not 0 (a finished request)
  * seq_len becomes 0 and all its blocks go back, but for the first keep[r]
@@ -551,9 +553,13 @@ int sd_token_counts(hipStream_t stream, int R, int V, const int32_t* tokens, lon
  *   ell        [R] sd_slot_reserve's ell_out;  free_count: its free_left
  *   n_accepted [R], out_tokens [R][q_max] sd_verify's (q_max = gamma_max + 1)
  *   release, keep  [R] int32 or NULL
- *   status     [R] int32 or NULL, sd_verify's; BAD_INPUT is added where
- *              seq_len or ell is out of range (the request stays as it is)
- *              or more blocks come back than the pool holds (dropped)
+ *   status     [R] int32 or NULL: the bits of the step's calls, OR-ed.  Rows
+ *              without slots (sd_slot_reserve's BAD_INPUT) or left unshaped
+ *              (sd_logit_shape's) pass sd_verify like others, which cannot
+ *              know: give their bits here beside sd_verify's, or what it
+ *              drew from them is kept.  BAD_INPUT is added where seq_len or
+ *              ell is out of range (the request stays as it is) or more
+ *              blocks come back than the pool holds (dropped)
  *   seq_len_out [R] int64 (usable as pos0 of the random decisions), n_new
  *   [R] int32, free_count_out [1]; x0_out [R] int32 or NULL: the next anchors
  *   out_tokens[r][n_accepted[r]] (x0[r] where n_new is 0).  seq_len_out,

@@ -15,6 +15,7 @@ from (request, position) holds.
 import numpy as np
 
 BAD_INPUT, NO_SLOT = 32, 64
+HELD = 2 | 4 | BAD_INPUT   # a step of such a status is repeated
 
 
 def blocks_of(n, block_size):
@@ -101,7 +102,7 @@ def commit(seq_len, ell, n_acc, table, free_list, free_count, block_size, q_max,
                 status[r] |= BAD_INPUT
             continue
         acc = min(max(int(n_acc[r]), 0), max(L, 0))
-        n_new = acc + 1 if q and not st & 6 else 0
+        n_new = acc + 1 if q and not st & HELD else 0
         held = blocks_of(n0 + q, block_size)
         if release is not None and release[r]:
             new, kept = 0, min(max(0 if keep is None else int(keep[r]), 0), held)
