@@ -630,6 +630,18 @@ extern "C" int sd_logit_shape(hipStream_t stream, int R, int gamma_max, int V, i
   const int groups = spare < 1 ? 1 : (spare < rows ? (int)spare : rows);
   a.group = (rows + groups - 1) / groups;
   if (items * groups > 0xFFFFFFFFLL / kShapeThreads) return SD_EUNSUPPORTED;  // work-items of one launch
+  using sdv::span;
+  const long long es = dtype == SD_DTYPE_BF16 ? 2 : 4;
+  const sdv::Span written[] = {span(out, n_rows, V * es, ld * es), span(status, 4LL * R)};
+  const sdv::Span read[] = {
+      span(logits == out ? nullptr : logits, n_rows, V * es, ld * es), span(row0, 4LL * R), span(ell, 4LL * R),
+      span(draft_tokens, 4LL * R * gamma_max), span(repetition, 4LL * R), span(frequency, 4LL * R),
+      span(presence, 4LL * R), span(pen ? seen : nullptr, n_slots, 4LL * words, 4LL * ld_seen),
+      span(pen ? counts : nullptr, n_slots, 4LL * V, 4LL * ld_counts), span(slot, 4LL * R),
+      span(bias_off, 8LL * (R + 1LL)), span(bias_off ? bias_tok : nullptr, 4 * n_bias),
+      span(bias_off ? bias_val : nullptr, 4 * n_bias),
+      span(mask_row0 ? mask : nullptr, n_mask_rows, 4LL * words, 4LL * ld_mask), span(mask_row0, 4LL * R)};
+  if (sdv::overlap(written, read)) return SD_EINVAL;
   const dim3 g((unsigned)items, groups), b(kShapeThreads);
   hipError_t e;
   if (dtype == SD_DTYPE_BF16)
@@ -654,6 +666,13 @@ extern "C" int sd_token_counts(hipStream_t stream, int R, int V, const int32_t* 
   if (start && !length) return SD_EINVAL;
   if (!start && (long long)R * width > n_tokens) return SD_ERANGE;
   if ((long long)R * kCountThreads > 0xFFFFFFFFLL) return SD_EUNSUPPORTED;
+  using sdv::span;
+  const sdv::Span written[] = {span(seen, n_slots, (V + 31) / 32 * 4LL, 4LL * ld_seen),
+                               span(counts, n_slots, 4LL * V, 4LL * ld_counts), span(status, 4LL * R)};
+  const sdv::Span read[] = {span(tokens, n_tokens < 1LL << 60 ? 4 * n_tokens : 1LL << 62),
+                            span(start, 8LL * R), span(length, 4LL * R), span(prompt_len, 4LL * R),
+                            span(slot, 4LL * R), span(reset, 4LL * R)};
+  if (sdv::overlap(written, read)) return SD_EINVAL;
   CountArgs a;
   a.tokens = tokens;
   a.start = start;

@@ -520,6 +520,18 @@ extern "C" int sd_slot_reserve(hipStream_t stream, int R, int q_max, int block_s
   if (R > 0 && row_token && ld_tokens < (x0 ? q_max - 1 : q_max)) return SD_ERANGE;
   if (!workspace || workspace_bytes < sd_slot_reserve_workspace_size(R)) return SD_ERANGE;
   if (((uintptr_t)workspace & 7) != 0) return SD_EINVAL;
+  using sdv::span;
+  const long long per = 4LL * R;   // bytes of an int32 per request
+  const sdv::Span written[] = {
+      span(block_table, per * max_blocks), span(ell_out, per), span(row0, per), span(cu_rows, per + 4),
+      span(ctx_len, per), span(batch, 4), span(free_left, 4), span(row_req, 4LL * max_rows),
+      span(row_pos, 4LL * max_rows), span(row_slot, 8LL * max_rows), span(row_token, 4LL * max_rows),
+      span(status, per), span(workspace, 3 * per + 4)};
+  const sdv::Span read[] = {
+      span(seq_len, 2 * per), span(ell == ell_out ? nullptr : ell, per), span(row_token ? x0 : nullptr, per),
+      span(row_token ? tokens : nullptr, R, 4LL * (x0 ? q_max - 1 : q_max), 4LL * ld_tokens),
+      span(free_list, 4LL * n_blocks), span(free_count == free_left ? nullptr : free_count, 4)};
+  if (sdv::overlap(written, read)) return SD_EINVAL;
   ReserveArgs a;
   a.seq_len = seq_len;
   a.ell = ell;
@@ -589,6 +601,17 @@ extern "C" int sd_slot_commit(hipStream_t stream, int R, int q_max, int block_si
   if (R > 0 && x0_out && (!out_tokens || !x0)) return SD_EINVAL;
   if (!workspace || workspace_bytes < sd_slot_commit_workspace_size(R)) return SD_ERANGE;
   if (((uintptr_t)workspace & 7) != 0) return SD_EINVAL;
+  using sdv::span;
+  const long long per = 4LL * R;   // bytes of an int32 per request
+  const sdv::Span written[] = {span(free_list, 4LL * n_blocks), span(status, per),  span(seq_len_out, 2 * per),
+                               span(x0_out, per),               span(n_new, per),   span(free_count_out, 4),
+                               span(workspace, 3 * per)};
+  const sdv::Span read[] = {
+      span(seq_len == seq_len_out ? nullptr : seq_len, 2 * per), span(ell, per), span(n_accepted, per),
+      span(x0_out ? out_tokens : nullptr, per * q_max), span(x0_out && x0 != x0_out ? x0 : nullptr, per),
+      span(release, per), span(keep, per), span(block_table, per * max_blocks),
+      span(free_count == free_count_out ? nullptr : free_count, 4)};
+  if (sdv::overlap(written, read)) return SD_EINVAL;
   CommitArgs a;
   a.seq_len = seq_len;
   a.ell = ell;

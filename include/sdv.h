@@ -52,6 +52,10 @@
  *     multiple of 8 so that every row starts 16-byte aligned); only the first
  *     V entries of a row are read.  V must be a multiple of 8.
  *   - bf16 data is passed as raw 16-bit patterns (uint16_t).
+ *   - What a call writes (outputs, state, workspace) overlaps none of its other
+ *     arguments, unless its text names them; sd_logit_shape, sd_token_counts,
+ *     sd_slot_reserve and sd_slot_commit return SD_EINVAL where it does, by the
+ *     sizes given.
  */
 #ifndef SDV_H
 #define SDV_H

@@ -91,3 +91,31 @@ def test_loop_holds_refused_requests():
     L.m0[4] = 4 * Q
     s, z, v, c, status = _step(L)
     assert (c["n_new"] == v["n_acc"] + 1).all() and ((s["status"] | z["status"]) & 32 == 0).all()
+
+
+def test_overlapping_outputs_are_refused():
+    """Refused on the host, whatever the kernel chosen; the in-place forms that
+    the interface names are not."""
+    i = lambda *k: torch.zeros(k, dtype=torch.int32, device=DEV)  # noqa: E731
+    n, q = 9, 3
+    seq, acc, tok, x0, table, free, F = torch.zeros(n, dtype=torch.int64, device=DEV), i(n), i(n, q), i(n), i(n, 4), \
+        i(40), i(1)
+    for out in (dict(n_new=acc), dict(x0=acc), dict(n_new=x0, x0=x0), dict(free_count=free[:1])):
+        with pytest.raises(sdv.SdvError):
+            sdv.sd_slot_commit(seq, i(n) - 1, acc, table, free, F, 16, out_tokens=tok, x0=x0, out=out)
+    sdv.sd_slot_commit(seq, i(n) - 1, acc, table, free, F, 16, out_tokens=tok, x0=x0,
+                       out=dict(seq_len=seq, x0=x0, free_count=F))
+    ell = i(n) - 1
+    for out in (dict(ctx_len=ell), dict(status=ell), dict(batch=F), dict(row0=x0), dict(row_token=tok.view(-1))):
+        with pytest.raises(sdv.SdvError):
+            sdv.sd_slot_reserve(seq, ell, table, free, F, 16, q, x0=x0, tokens=tok, out=out)
+    sdv.sd_slot_reserve(seq, ell, table, free, F, 16, q, x0=x0, tokens=tok, out=dict(ell=ell, free_count=F))
+    x = torch.zeros((2 * n, 64), device=DEV)
+    row0, none = i(n), i(n) - 1
+    with pytest.raises(sdv.SdvError):
+        sdv.sd_logit_shape(x[:n], row0, none, 64, gamma_max=0, out=dict(logits=x[1:n + 1]))
+    with pytest.raises(sdv.SdvError):
+        sdv.sd_logit_shape(x, row0, none, 64, gamma_max=0, out=dict(status=none))
+    sdv.sd_logit_shape(x[:n], row0, none, 64, gamma_max=0, out=dict(logits=x[n:]))
+    with pytest.raises(sdv.SdvError):
+        sdv.sd_token_counts(tok, i(n, 2), i(n, 64), 64, length=acc, out=dict(status=acc))
