@@ -638,8 +638,9 @@ extern "C" int sd_logit_shape(hipStream_t stream, int R, int gamma_max, int V, i
   const bool copy = out != logits;
   const bool nt = (double)R * rows * a.ld_bytes * (copy ? 2 : 1) > kCacheBytes;
   const long long spare = kFullWaves / (items > 0 ? items : 1);   // waves a request's rows may be split over
-  const int groups = spare < 1 ? 1 : (spare < rows ? (int)spare : rows);
-  a.group = (rows + groups - 1) / groups;
+  const int most = spare < 1 ? 1 : (spare < rows ? (int)spare : rows);
+  a.group = (rows + most - 1) / most;
+  const int groups = (rows + a.group - 1) / a.group;   // each with rows of its own
   if (items * groups > 0xFFFFFFFFLL / kShapeThreads) return SD_EUNSUPPORTED;  // work-items of one launch
   using sdv::span;
   const long long es = dtype == SD_DTYPE_BF16 ? 2 : 4;
