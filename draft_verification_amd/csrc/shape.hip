@@ -17,16 +17,17 @@ constexpr int kShapeThreads = 64;
 constexpr int kVecTokens = 8;                              // tokens per thread: one mask byte
 constexpr int kShapeChunk = kShapeThreads * kVecTokens;    // tokens per workgroup
 // A batch with fewer (request, chunk) waves, two rounds of what the chip holds
-// at this kernel's registers, splits its rows over more (64 requests, V =
-// 32000: 15 us split in two, 21 us unsplit; 4 requests, V = 1000: 4.0 and 8.5
-// us; 16 requests with 9 rows, V = 151936: 20.3 us, 23.6 us with one round; a
-// batch that fills the chip anyway loses 100 us of 460 by a split in two).
+// at this kernel's registers, splits its rows over more (64 requests with 9
+// rows, V = 32000: 13.1 us in 3 groups, 17.2 us unsplit, 13.9 us in 5; 4
+// requests with 5 rows, V = 1000: 3.8 and 7.5 us; 16 requests with 9 rows, V =
+// 151936: 12.4 us, 16.5 us with half as many waves).  One that fills the chip
+// anyway gains 1 % at most by a split and is left whole: its state is read once.
 constexpr long long kFullWaves = 16384;
 // Beyond this the rows do not stay in the 256 MB last-level cache: they are
-// streamed past it and wait for their masks (512 requests, V = 151936: 461 us
-// streamed, 548 us not; 64 requests, V = 32000: 17.1 and 15.9 us).
+// streamed past it and wait for their masks (512 requests, V = 151936: 426 us
+// streamed, 560 us not; 64 requests, V = 32000: 14.5 and 13.1 us).
 constexpr double kCacheBytes = 128 << 20;
-constexpr int kWholeLanes = 32;   // (grammars in place: 64 us, 72 us vector by vector)
+constexpr int kWholeLanes = 32;   // (grammars in place: 63 us, 71 us vector by vector; penalties: 227 and 223 us)
 
 struct ShapeArgs {
   const char* logits;
@@ -122,15 +123,8 @@ struct Request {
   int row0, srow, m0;
   int64_t b0, b1;
   float rep, freq, pres;
-  float inv;       // 1 / rep
-  uint32_t near;   // see penalised
   bool pen, ok;
 };
-constexpr uint32_t kNearMin = 0x0D800000u;   // 2^-100
-SDV_DEV uint32_t near_range(float rep) {
-  if (!(rep >= 0x1p-126f && rep <= 0x1p126f)) return 0;
-  return __float_as_uint(rep >= 1.0f ? __builtin_huge_valf() : rep * 0x1p127f) - kNearMin;
-}
 SDV_DEV Request read_request(const ShapeArgs& a, int r) {
   Request q;   // requested together
   q.n = min(a.ell[r], a.gmax) + 1;
@@ -143,8 +137,6 @@ SDV_DEV Request read_request(const ShapeArgs& a, int r) {
   q.b0 = a.bias_off ? a.bias_off[r] : 0;
   q.b1 = a.bias_off ? a.bias_off[r + 1] : 0;
   const float inf = __builtin_huge_valf();
-  q.inv = 1.0f / q.rep;
-  q.near = near_range(q.rep);
   q.pen = q.rep != 1.0f || q.freq != 0.0f || q.pres != 0.0f;
   q.ok = q.row0 >= 0 && (int64_t)q.row0 + q.n <= a.n_rows;
   q.ok = q.ok && q.rep > 0.0f && q.rep < inf && fabsf(q.freq) < inf && fabsf(q.pres) < inf;
@@ -152,22 +144,6 @@ SDV_DEV Request read_request(const ShapeArgs& a, int r) {
   q.ok = q.ok && (q.m0 < 0 || (int64_t)q.m0 + q.n <= a.n_mask_rows);
   q.ok = q.ok && q.b0 >= 0 && q.b0 <= q.b1 && q.b1 <= a.n_bias;
   return q;
-}
-
-// y / rep where y > 0, else y * rep.  The quotient is y * inv and one step of
-// correction, u + inv * (y - u * rep): u is within 1.5 units of it and the
-// difference within 2^-24 of itself, so the corrected sum is within 2^-22 of a
-// unit before its rounding (waves with many seen tokens are bound by
-// instructions: the divide's own sequence took 14.4 us where this takes 13.8,
-// for 64 requests at V = 32000).  That holds while inv is a normal number and
-// the difference's lowest bit, some 2^-47 of y, no smaller than 2^-149.  A y
-// below kNearMin, one whose u may overflow and any y of an extreme rep are
-// divided: q.near is the range of bit patterns from kNearMin on that are not,
-// so that one comparison tells (two of floats: 13.6 us where this takes 13.3).
-SDV_DEV float penalised(const Request& q, float y) {
-  const float u = y * (y > 0.0f ? q.inv : q.rep);
-  if (__float_as_uint(y) - kNearMin < q.near) return fmaf(fmaf(-u, q.rep, y), q.inv, u);
-  return y > 0.0f ? y / q.rep : u;
 }
 
 // What a lane holds for its eight tokens v0..v0+7.
@@ -201,7 +177,10 @@ struct Tokens {
       if ((hit >> e) & 1) {
         float y = x.get(e);
         if ((met >> e) & 1) {
-          y = penalised(q, y);
+          // (the division as it is: a reciprocal and one step of correction, which
+          // needs cases of its own where they underflow, took 13.3 us where
+          // this takes 13.1, for 64 requests at V = 32000)
+          y = y > 0.0f ? y / q.rep : y * q.rep;
           y = fmaf(-q.freq, c[e], y) - (c[e] > 0.0f ? q.pres : 0.0f);
         }
         if ((biased >> e) & 1) y += bias[e];
@@ -234,9 +213,9 @@ SDV_DEV void report(const ShapeArgs& a, int r, const int32_t* drafts, int n, int
 // 251 us, half of what it takes out of place.
 template <bool BF16, bool NT, bool COPY>
 __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
-  // rows whose loads are issued together (large batch out of place: 1: 469 us,
-  // 2: 463 us, 4: 486 us; in place 2: 70 us, 4: 67 us; 64 requests at V =
-  // 32000 1: 14.9 us, 2: 15.9 us)
+  // rows whose loads are issued together (large batch out of place: 1: 440 us,
+  // 2: 426 us, 4: 422 us with more registers; grammars in place 1: 66 us, 2: 67
+  // us, 4: 63 us; 64 requests at V = 32000 1: 13.1 us, 2: 14.1 us)
   constexpr int kRows = NT ? (COPY ? 2 : 4) : 1;
   __shared__ int last[kShapeChunk];   // 1 + index of a token's last bias entry
   const int r = blockIdx.x / a.n_ch, ch = blockIdx.x % a.n_ch;
