@@ -489,6 +489,14 @@ def _arg(t, dtype, name, index, n=None):
     raise ValueError(f"{name} must hold {n} elements, got shape {list(t.shape)}")
 
 
+def _fits(fn, sizes):
+    """Refuse sizes that the C interface's int does not hold, which ctypes
+    would cut to their low 32 bits.  `sizes`: all of them, OR-ed together (a
+    negative one is refused there)."""
+    if sizes >> 31 not in (0, -1):
+        raise SdvError(fn, SD_EUNSUPPORTED)
+
+
 def _state_rows(seen, counts, V):
     """(n_slots, ld_seen, ld_counts) of a token state; 0 where there is none."""
     if seen is None:
@@ -544,16 +552,18 @@ def sd_logit_shape(logits, row0, ell, V, gamma_max=None, draft_tokens=None, repe
     if dst.shape != logits.shape:
         raise ValueError(f"out must have the logits' shape {list(logits.shape)}, got {list(dst.shape)}")
     i32, f32, ldt = torch.int32, torch.float32, logits.dtype
+    V, gamma_max = int(V), int(gamma_max)
+    m_rows, m_ld = (0, 0) if mask is None else mask.shape
+    _fits("sd_logit_shape", R | gamma_max | V | ld | n_rows | n_slots | ld_seen | ld_counts | m_rows | m_ld)
     code = lib().sd_logit_shape(
-        _raw_stream(dev), R, int(gamma_max), int(V), ld, dt, _arg(logits, ldt, "logits", dev),
+        _raw_stream(dev), R, gamma_max, V, ld, dt, _arg(logits, ldt, "logits", dev),
         _arg(dst, ldt, "out", dev), n_rows, _arg(row0, i32, "row0", dev), _arg(ell, i32, "ell", dev, R),
         _arg(draft_tokens, i32, "draft_tokens", dev, R * gamma_max), _arg(repetition, f32, "repetition", dev, R),
         _arg(frequency, f32, "frequency", dev, R), _arg(presence, f32, "presence", dev, R),
         _arg(seen, i32, "seen", dev), ld_seen, _arg(counts, i32, "counts", dev), ld_counts, n_slots,
         _arg(slot, i32, "slot", dev, R), _arg(b_off, torch.int64, "bias offsets", dev, R + 1),
         _arg(b_tok, i32, "bias tokens", dev), _arg(b_val, f32, "bias values", dev, n_bias), n_bias,
-        _arg(mask, i32, "mask", dev), 0 if mask is None else mask.shape[1],
-        0 if mask is None else mask.shape[0], _arg(mask_row0, i32, "mask_row0", dev, R),
+        _arg(mask, i32, "mask", dev), m_ld, m_rows, _arg(mask_row0, i32, "mask_row0", dev, R),
         _arg(status, i32, "status", dev, R))
     _check("sd_logit_shape", code)
     return dict(logits=dst, status=status)
@@ -585,9 +595,10 @@ def sd_token_counts(tokens, seen, counts, V, start=None, length=None, prompt_len
         raise ValueError("seen is needed")
     n_slots, ld_seen, ld_counts = _state_rows(seen, counts, V)
     status = out["status"] if out and "status" in out else torch.empty(R, dtype=torch.int32, device=tokens.device)
-    i32 = torch.int32
+    i32, V = torch.int32, int(V)
+    _fits("sd_token_counts", R | V | width | n_slots | ld_seen | ld_counts)
     code = lib().sd_token_counts(
-        _raw_stream(dev), R, int(V), _arg(tokens, i32, "tokens", dev), tokens.numel(), width,
+        _raw_stream(dev), R, V, _arg(tokens, i32, "tokens", dev), tokens.numel(), width,
         _arg(start, torch.int64, "start", dev), _arg(length, i32, "length", dev, R),
         _arg(prompt_len, i32, "prompt_len", dev, R), _arg(slot, i32, "slot", dev, R),
         _arg(reset, i32, "reset", dev, R), _arg(seen, i32, "seen", dev), ld_seen,
@@ -615,11 +626,12 @@ def sd_slot_reserve(seq_len, ell, block_table, free_list, free_count, block_size
     R = seq_len.numel()
     if block_table.dim() != 2 or (tokens is not None and tokens.dim() != 2):
         raise ValueError("block_table and tokens must be 2-D")
-    mb = block_table.shape[1]
+    mb, n_blocks, ld_tokens = block_table.shape[1], free_list.numel(), 0 if tokens is None else tokens.shape[1]
     o = out or {}
-    i32 = torch.int32
+    i32, q_max, block_size = torch.int32, int(q_max), int(block_size)
     if max_rows is None:
         max_rows = o["row_req"].numel() if "row_req" in o else R * q_max
+    _fits("sd_slot_reserve", R | q_max | block_size | mb | n_blocks | max_rows | ld_tokens)
     i64 = torch.int64
     make = lambda k, n, dt=i32: o[k] if k in o else torch.empty(n, dtype=dt, device=device)  # noqa: E731
     res = dict(ell=make("ell", R), row0=make("row0", R), cu_rows=make("cu_rows", R + 1), ctx_len=make("ctx_len", R),
@@ -629,10 +641,9 @@ def sd_slot_reserve(seq_len, ell, block_table, free_list, free_count, block_size
                status=make("status", R))
     ws = workspace if workspace is not None else _workspace(sd_slot_reserve_workspace_size(R), device)
     code = lib().sd_slot_reserve(
-        _raw_stream(dev), R, int(q_max), int(block_size), mb, free_list.numel(), max_rows, 1 if padded else 0,
+        _raw_stream(dev), R, q_max, block_size, mb, n_blocks, max_rows, 1 if padded else 0,
         _arg(seq_len, i64, "seq_len", dev), _arg(ell, i32, "ell", dev, R), _arg(x0, i32, "x0", dev, R),
-        _arg(tokens, i32, "tokens", dev, None if tokens is None else R * tokens.shape[1]),
-        0 if tokens is None else tokens.shape[1], _arg(block_table, i32, "block_table", dev, R * mb),
+        _arg(tokens, i32, "tokens", dev, R * ld_tokens), ld_tokens, _arg(block_table, i32, "block_table", dev, R * mb),
         _arg(free_list, i32, "free_list", dev), _arg(free_count, i32, "free_count", dev, 1),
         _arg(res["ell"], i32, "out ell", dev, R), _arg(res["row0"], i32, "row0", dev, R),
         _arg(res["cu_rows"], i32, "cu_rows", dev, R + 1), _arg(res["ctx_len"], i32, "ctx_len", dev, R),
@@ -673,6 +684,8 @@ def sd_slot_commit(seq_len, ell, n_acc, block_table, free_list, free_count, bloc
         q_max = out_tokens.shape[1]
     elif q_max is None:
         raise ValueError("q_max is needed without out_tokens")
+    n_blocks, q_max, block_size = free_list.numel(), int(q_max), int(block_size)
+    _fits("sd_slot_commit", R | q_max | block_size | mb | n_blocks)
     o = out or {}
     i32 = torch.int32
     i64 = torch.int64
@@ -681,7 +694,7 @@ def sd_slot_commit(seq_len, ell, n_acc, block_table, free_list, free_count, bloc
                x0=None if out_tokens is None else make("x0", R))
     ws = workspace if workspace is not None else _workspace(sd_slot_commit_workspace_size(R), device)
     code = lib().sd_slot_commit(
-        _raw_stream(dev), R, int(q_max), int(block_size), mb, free_list.numel(),
+        _raw_stream(dev), R, q_max, block_size, mb, n_blocks,
         _arg(seq_len, i64, "seq_len", dev), _arg(ell, i32, "ell", dev, R), _arg(n_acc, i32, "n_acc", dev, R),
         _arg(out_tokens, i32, "out_tokens", dev, R * q_max), _arg(x0, i32, "x0", dev, R),
         _arg(release, i32, "release", dev, R), _arg(keep, i32, "keep", dev, R),
