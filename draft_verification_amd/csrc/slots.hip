@@ -401,7 +401,7 @@ SDV_DEV void commit_scan(const CommitArgs& a, uint64_t* part, int* free_out, Emi
     int gives = 0;
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
-      const int q = L[k] < 0 ? 0 : L[k] + 1;
+      const int q = L[k] < 0 || L[k] >= a.q_max ? 0 : L[k] + 1;
       c[k] = Committed{len[k], 0, 0, 0, 0, 0, false};
       if (len[k] < 0 || len[k] > cap || L[k] >= a.q_max || len[k] + q > cap) {
         c[k].bad = true;

@@ -44,6 +44,17 @@ def test_more_blocks_than_the_pool_holds(n):
                 g.integers(0, 99, (n, q)), g.integers(0, 99, n), status, (g.random(n) < 0.1).astype(int))
 
 
+def test_commit_of_the_largest_ell():
+    """ell + 1 is formed of an ell in range only."""
+    top = (1 << 31) - 1
+    g = np.random.default_rng(2)
+    seq, ell = np.array([3, 3, 8, 0]), np.array([top, 2, top, top])
+    table, free, F = _pool(g, 4, 4, np.array([1, 2, 2, 0]), 3)
+    for alias in (False, True):
+        want = _commit(seq, ell, np.array([1, 1, top, 0]), table, free, F, 4, 5, status=np.zeros(4, np.int32), alias=alias)
+        assert want["n_new"].tolist() == [0, 2, 0, 0]
+
+
 def _step(L):
     """Loop.step with the statuses of all its calls handed on."""
     s = sdv.sd_slot_reserve(L.seq, L.ell, L.table, L.free, L.F, BS, Q, x0=L.x0, tokens=L.drafts)
