@@ -578,7 +578,8 @@ def sd_token_counts(tokens, seen, counts, V, start=None, length=None, prompt_len
     -1 behind sd_verify's tokens), with length [R] int32 or None; or any shape
     with start [R] int64 (into all of it) and length, of at most max_length
     where that is given: do so for short lists in a large buffer.  prompt_len [R] int32: how many leading tokens
-    of each list are prompt; reset [R] int32: clear the state row first.
+    of each list are prompt; reset [R] int32: clear the state row first (for
+    calls that start requests: with it short lists take many times as long).
     Returns a dict: status."""
     dev = tokens.get_device()
     if start is not None:

@@ -207,10 +207,13 @@ SDV_DEV void report(const ShapeArgs& a, int r, const int32_t* drafts, int n, int
 // fastest (448 us, 455 us with two and 481 us with four waves).  NT: a batch
 // that does not fit the last-level cache.
 // Measured: 512 requests with up to 17 rows each, V = 151936 bf16, out of
-// place, every term: 430 us for 2.46 GB of memory traffic, 5.7 TB/s (a plain
-// copy reaches 4.9); grammars in place, 128 requests, V = 129280: 63.5 us,
-// 0.30 GB, 4.7 TB/s (partial lines); penalties alone in place, 512 requests:
-// 251 us, half of what it takes out of place.
+// place, every term: 426 us for 2.46 GB of memory traffic, 5.8 TB/s (a copy of
+// 2 GiB with streaming accesses reaches 6.5, torch's 4.9); grammars in place,
+// 128 requests, V = 129280: 56-63 us by the share of masked rows, 0.30 GB,
+// 4.7 TB/s (partial lines); penalties alone, 512 requests with histories of up
+// to 1500 tokens: 227 us in place, 0.36 GB (single 16-byte pieces of lines),
+// 518 us out of place; fp32 out of place, 256 requests, penalties: 642 us, 3.2
+// GB, 4.9 TB/s.
 template <bool BF16, bool NT, bool COPY>
 __global__ __launch_bounds__(kShapeThreads) void k_logit_shape(ShapeArgs a) {
   // rows whose loads are issued together (large batch out of place: 1: 440 us,
@@ -412,7 +415,9 @@ __global__ __launch_bounds__(kCountThreads) void k_count_clear(CountArgs a) {
 // Measured at V = 151936: 96 lists of up to 131072 tokens 26 us (252 us with a
 // clearing pass and atomics on the state, 1.8 ms where half of a list is one
 // token, here 34 us); one list of 131072 tokens 14.6 us; 256 lists of at most
-// 100 tokens 32 us, 5.0 TB/s.
+// 100 tokens 32 us, 5.0 TB/s.  A call that has `reset` pays for the ranges also
+// where no request resets (512 lists of up to 17 tokens: 51 us, 2.4 us added by
+// atomics without it).
 constexpr int kOwnThreads = 1024;
 constexpr int kOwnLoads = 16;            // 4: 30 us, 8: 27 us for the 96 lists
 constexpr int kOwnMaxChunk = 32768;      // 128 KB of the 160 KB of LDS

@@ -440,10 +440,10 @@ int sd_uniforms(hipStream_t stream, uint64_t seed, long long n, const int64_t* r
  *
  *   R, gamma_max, V, ld, dtype as sd_verify; ell < 0: the request has no rows
  *   logits, out  [n_rows][ld], 16-byte aligned; the rows of different
- *                requests do not overlap; out may be logits (only the touched
- *                parts of a row are then read and written), else the two do
- *                not overlap and rows outside the batch and entries past V
- *                are left as they are in out
+ *                requests do not overlap; out may be logits (logits that no
+ *                term touches keep their bits, but may be read and written
+ *                back), else the two do not overlap; rows outside the batch
+ *                and entries past V are left as they are in out
  *   draft_tokens [R][gamma_max] int32, or NULL: no draft counts as written
  *   repetition (finite, > 0), frequency, presence (finite)  [R] fp32, each
  *                NULL for 1, 0 and 0
@@ -491,7 +491,10 @@ int sd_logit_shape(hipStream_t stream, int R, int gamma_max, int V, int ld, int 
  *   range.  sd_verify's out_tokens are lists of width gamma_max + 1.
  *   prompt_len [R] int32 or NULL (0): prompt tokens are seen, not counted
  *   reset      [R] int32 or NULL: where not 0 the state row is cleared first
- *              (whatever it held)
+ *              (whatever it held).  Give it to calls that start requests: with
+ *              it the ranges of every request's row are walked, also where it
+ *              is 0 (512 lists of up to 17 tokens, V = 151936: 51 us, 2.4 us
+ *              without)
  *   seen, counts (or NULL), their leading dimensions, n_slots, slot as
  *   sd_logit_shape; requests may share a state row
  *   status [R] int32 out: BAD_INPUT where the list or the slot is out of
