@@ -524,7 +524,7 @@ extern "C" int sd_slot_reserve(hipStream_t stream, int R, int q_max, int block_s
   const long long per = 4LL * R;   // bytes of an int32 per request
   const sdv::Span written[] = {
       span(block_table, per * max_blocks), span(ell_out, per), span(row0, per), span(cu_rows, per + 4),
-      span(ctx_len, per), span(batch, 4), span(free_left, 4), span(row_req, 4LL * max_rows),
+      span(ctx_len, per), span(batch == cu_rows + R ? nullptr : batch, 4), span(free_left, 4), span(row_req, 4LL * max_rows),
       span(row_pos, 4LL * max_rows), span(row_slot, 8LL * max_rows), span(row_token, 4LL * max_rows),
       span(status, per), span(workspace, 3 * per + 4)};
   const sdv::Span read[] = {

@@ -545,7 +545,8 @@ int sd_token_counts(hipStream_t stream, int R, int V, const int32_t* tokens, lon
  *              rows, ctx_len 0) or a block id is outside [0, n_blocks) (its
  *              rows have slot -1; see sd_slot_commit's status)
  * ell_out may be ell and free_left may be free_count (for more than one
- * workgroup's rows this takes two launches); seq_len is not changed, so a
+ * workgroup's rows this takes two launches), and batch may be cu_rows + R;
+ * seq_len is not changed, so a
  * step that is not committed is repeated by passing the old free_count.
  * R = 0 writes the totals and the rows alone.
  *
@@ -560,7 +561,7 @@ int sd_token_counts(hipStream_t stream, int R, int V, const int32_t* tokens, lon
  *   ell        [R] sd_slot_reserve's ell_out;  free_count: its free_left
  *   n_accepted [R], out_tokens [R][q_max] sd_verify's (q_max = gamma_max + 1)
  *   release, keep  [R] int32 or NULL
- *   status     [R] int32 or NULL: the bits of the step's calls, OR-ed.  Rows
+ *   status     [R] int32 or NULL: the bits of this step's calls, OR-ed.  Rows
  *              without slots (sd_slot_reserve's BAD_INPUT) or left unshaped
  *              (sd_logit_shape's) pass sd_verify like others, which cannot
  *              know: give their bits here beside sd_verify's, or what it

@@ -121,6 +121,10 @@ def test_overlapping_outputs_are_refused():
         with pytest.raises(sdv.SdvError):
             sdv.sd_slot_reserve(seq, ell, table, free, F, 16, q, x0=x0, tokens=tok, out=out)
     sdv.sd_slot_reserve(seq, ell, table, free, F, 16, q, x0=x0, tokens=tok, out=dict(ell=ell, free_count=F))
+    cu = i(n + 1) + 9
+    got = sdv.sd_slot_reserve(seq, i(n), i(n, 4), torch.arange(40, dtype=torch.int32, device=DEV), i(1) + 40, 16, q,
+                              out=dict(cu_rows=cu, batch=cu[n:]))
+    assert cu.tolist() == list(range(n + 1)) and got["batch"].tolist() == [n]
     x = torch.zeros((2 * n, 64), device=DEV)
     row0, none = i(n), i(n) - 1
     with pytest.raises(sdv.SdvError):

@@ -102,6 +102,14 @@ def test_rows_side_by_side_in_one_buffer():
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="addresses that do not exist: only where nothing can be launched")
+def test_the_batch_may_end_the_prefix_sums():
+    at = {k: (i + 1) << 20 for i, k in enumerate(RESERVE)}
+    assert _call("reserve", dict(at, batch=at["cu"] + 4 * R)) == _lib.SD_ELAUNCH
+    assert _call("reserve", dict(at, batch=at["cu"])) == _lib.SD_EINVAL
+    assert _call("reserve", dict(at, batch=at["cu"] + 4 * R, row_pos=at["cu"])) == _lib.SD_EINVAL
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="addresses that do not exist: only where nothing can be launched")
 def test_an_unbounded_list_length_meets_no_other_allocation_below():
     """n_tokens near 2^63 does not wrap round."""
     call = lambda seen: sdv.lib().sd_token_counts(  # noqa: E731
