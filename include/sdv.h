@@ -545,16 +545,14 @@ int sd_token_counts(hipStream_t stream, int R, int V, const int32_t* tokens, lon
  *              rows, ctx_len 0) or a block id is outside [0, n_blocks) (its
  *              rows have slot -1; see sd_slot_commit's status)
  * ell_out may be ell and free_left may be free_count (for more than one
- * workgroup's rows this takes two launches), and batch may be cu_rows + R;
- * seq_len is not changed, so a
- * step that is not committed is repeated by passing the old free_count.
- * R = 0 writes the totals and the rows alone.
+ * workgroup's rows this takes two launches), and batch may be cu_rows + R.
+ * seq_len is not changed, so a step that is not committed is repeated by
+ * passing the old free_count.  R = 0 writes the totals and the rows alone.
  *
  * sd_slot_commit - after verification: n_new[r] = 1 + min(n_accepted[r],
  * ell[r]) tokens of the step stay (0 where ell[r] < 0 or status[r] has
  * NONFINITE, ZERO_Z or BAD_INPUT: the step is repeated), seq_len grows by
- * n_new, and the
- * blocks past the new length go back, request after request, to
+ * n_new, and the blocks past the new length go back, request after request, to
  * free_list[free_count..].  Where release[r] is not 0 (a finished request)
  * seq_len becomes 0 and all its blocks go back, but for the first keep[r]
  * (shared with others).
