@@ -40,6 +40,9 @@ SD_ST_ZERO_Q = 16
 SD_ST_BAD_INPUT = 32
 SD_ST_NO_SLOT = 64
 
+SD_CACHE_BF16 = 0
+SD_CACHE_FP4 = 1
+
 EXPORTS = (
     "sd_abi_version", "sd_status_string", "sd_schedule_workspace_size", "sd_schedule",
     "sd_verify_workspace_size",
@@ -49,6 +52,7 @@ EXPORTS = (
     "sd_uniforms", "sd_verify_noalloc",
     "sd_logit_shape", "sd_token_counts", "sd_slot_reserve_workspace_size", "sd_slot_reserve",
     "sd_slot_commit_workspace_size", "sd_slot_commit",
+    "sd_qk_rope", "sd_cache_append", "sd_cache_read",
 )
 
 
@@ -124,6 +128,14 @@ def lib():
     L.sd_slot_commit.restype = _I
     L.sd_slot_commit.argtypes = [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                  _P, _P, _P, _SZ]
+    _F, _L = ctypes.c_float, ctypes.c_longlong
+    L.sd_qk_rope.restype = _I
+    L.sd_qk_rope.argtypes = [_P, _I, _I, _I, _P, _I, _L, _P, _I, _L, _P, _P, _P, _F, _P, _I, _I, _P, _L, _P, _L]
+    L.sd_cache_append.restype = _I
+    L.sd_cache_append.argtypes = [_P, _I, _I, _I, _P, _I, _L, _P, _L, _P, _L, _I, _P, _P, _P, _P, _F, _P, _I, _I, _P,
+                                  _L, _I, _I, _I, _P, _P, _P, _P]
+    L.sd_cache_read.restype = _I
+    L.sd_cache_read.argtypes = [_P, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _L, _P, _L]
     _lib = L
     return L
 
@@ -706,3 +718,162 @@ def sd_slot_commit(seq_len, ell, n_acc, block_table, free_list, free_count, bloc
         _arg(ws, torch.uint8, "workspace", dev), ws.numel())
     _check("sd_slot_commit", code)
     return res
+
+
+def _heads(t, dtype, name, index, shape=None):
+    """(address, leading dimension) of rows of heads [rows][heads][D] whose
+    heads and channels lie together (None: (NULL, 0)), such as a part of a
+    projection's rows."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must live on cuda:{index}, not {t.device}")
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be [rows][heads][D]{'' if shape is None else f' {list(shape)}'}, "
+                         f"got shape {list(t.shape)}")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
+        raise ValueError(f"{name}: the heads of a row must lie together, got strides {[s0, s1, s2]}")
+    # a single row's stride says nothing
+    return t.data_ptr(), s0 if n > 1 else -(-h * d // 8) * 8
+
+
+_ROW_TYPES = {torch.bfloat16: SD_DTYPE_BF16, torch.float32: SD_DTYPE_F32}
+
+
+def _row_type(t, name):
+    dt = _ROW_TYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be bf16 or fp32")
+    return dt
+
+
+def _rotation(inv_freq, pos, D, what):
+    """rot_dim of the frequencies, checked against the heads."""
+    if inv_freq is None:
+        return 0
+    if pos is None:
+        raise ValueError(f"inv_freq needs {what}")
+    if 2 * inv_freq.numel() > D:
+        raise ValueError(f"inv_freq holds {inv_freq.numel()} pairs, a head {D} channels")
+    return 2 * inv_freq.numel()
+
+
+def _cache_args(cache, index):
+    """(type, n_blocks, n_kv, block_size, D, addresses) of a cache: (k, v) in
+    bf16, or (k, v, k_scale, v_scale) uint8 in 4 bits."""
+    if not isinstance(cache, (tuple, list)) or len(cache) not in (2, 4):
+        raise ValueError("cache must be (k, v) or (k, v, k_scale, v_scale)")
+    k, v = cache[0], cache[1]
+    dt = torch.bfloat16 if len(cache) == 2 else torch.uint8
+    at = [_arg(k, dt, "k cache", index), _arg(v, dt, "v cache", index), None, None]
+    if k is None or v is None or k.dim() != 4 or k.shape != v.shape:
+        raise ValueError("the caches must be [n_blocks][n_kv][block_size][channels] and alike")
+    n_blocks, n_kv, bs, D = k.shape
+    if len(cache) == 4:
+        D *= 2
+        for i, name in ((2, "k_scale"), (3, "v_scale")):
+            at[i] = _arg(cache[i], dt, name, index)
+            if cache[i] is None or cache[i].shape != (n_blocks, n_kv, bs, D // 32):
+                raise ValueError(f"{name} must be [n_blocks][n_kv][block_size][D / 32]")
+    return (SD_CACHE_BF16 if len(cache) == 2 else SD_CACHE_FP4), n_blocks, n_kv, bs, D, at
+
+
+@_on_device
+def sd_qk_rope(q, k, pos, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, out=None, *,
+               stream=None):
+    """Norm and rotate the heads of queries and keys.  q [rows][n_q][D], k
+    [rows][n_kv][D] (or None) in bf16 or fp32, each row's heads together;
+    pos [rows] int32 (< 0: the row is left out; None without inv_freq);
+    inv_freq fp32, one frequency per pair of channels; q_weight, k_weight [D]
+    fp32 or None (no norm).  out["q"], out["k"] may be q and k themselves (in
+    place); without them new tensors are made, whose left-out rows are
+    undefined.  Returns a dict of device tensors: q, k."""
+    dev = q.get_device()
+    dt = _row_type(q, "q")
+    at_q, ld_q = _heads(q, q.dtype, "q", dev)
+    n, n_q, D = q.shape
+    n_k = 0 if k is None else k.shape[1] if k.dim() == 3 else -1
+    at_k, ld_k = _heads(k, q.dtype, "k", dev, None if k is None else (n, n_k, D))
+    o = out or {}
+    empty = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
+    qo = o["q"] if "q" in o else empty(q)
+    ko = o["k"] if "k" in o else empty(k)
+    at_qo, ld_qo = _heads(qo, q.dtype, "out q", dev, q.shape)
+    at_ko, ld_ko = (None, 0) if k is None else _heads(ko, q.dtype, "out k", dev, k.shape)
+    rot = _rotation(inv_freq, pos, D, "pos")
+    _fits("sd_qk_rope", n | n_q | n_k | D)
+    f32 = torch.float32
+    code = lib().sd_qk_rope(
+        _raw_stream(dev), n, D, dt, at_q, n_q, ld_q, at_k, n_k, ld_k, _arg(pos, torch.int32, "pos", dev, n),
+        _arg(q_weight, f32, "q_weight", dev, D), _arg(k_weight, f32, "k_weight", dev, D), float(eps),
+        _arg(inv_freq, f32, "inv_freq", dev), rot, 1 if interleaved else 0, at_qo, ld_qo, at_ko, ld_ko)
+    _check("sd_qk_rope", code)
+    return dict(q=qo, k=None if k is None else ko)
+
+
+@_on_device
+def sd_cache_append(k, v, cache, row_slot, row_pos=None, inv_freq=None, q=None, q_weight=None, k_weight=None, eps=1e-6,
+                    interleaved=False, out=None, *, stream=None):
+    """Put keys and values of a step's rows into their slots of a paged cache.
+    k, v [rows][n_kv][D] in bf16 or fp32, each row's heads together; cache:
+    (k, v) bf16 [n_blocks][n_kv][block_size][D], or (k, v, k_scale, v_scale)
+    uint8 [...][D / 2] and [...][D / 32] (4 bits), written in place; row_slot
+    [rows] int64 and row_pos [rows] int32 sd_slot_reserve's.  The keys are
+    normed and rotated as by sd_qk_rope on the way; with q [rows][n_q][D] so
+    are the queries, into out["q"] (which may be q) or a new tensor.  Returns
+    a dict: q (None without q)."""
+    dev = k.get_device()
+    dt = _row_type(k, "k")
+    at_k, ld_k = _heads(k, k.dtype, "k", dev)
+    n, n_kv, D = k.shape
+    at_v, ld_v = _heads(v, k.dtype, "v", dev, k.shape)
+    if v is None:
+        raise ValueError("v is needed")
+    n_q = 0 if q is None else q.shape[1] if q.dim() == 3 else -1
+    at_q, ld_q = _heads(q, k.dtype, "q", dev, None if q is None else (n, n_q, D))
+    qo = None
+    if q is not None:
+        qo = out["q"] if out and "q" in out else torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    at_qo, ld_qo = _heads(qo, k.dtype, "out q", dev, None if q is None else q.shape)
+    ctype, n_blocks, c_kv, bs, c_D, at = _cache_args(cache, dev)
+    if (c_kv, c_D) != (n_kv, D):
+        raise ValueError(f"the cache holds {c_kv} heads of {c_D} channels, k {n_kv} of {D}")
+    rot = _rotation(inv_freq, row_pos, D, "row_pos")
+    _fits("sd_cache_append", n | n_q | n_kv | D | n_blocks | bs)
+    f32 = torch.float32
+    code = lib().sd_cache_append(
+        _raw_stream(dev), n, D, dt, at_q, n_q, ld_q, at_k, ld_k, at_v, ld_v, n_kv,
+        _arg(row_pos, torch.int32, "row_pos", dev, n), _arg(row_slot, torch.int64, "row_slot", dev, n),
+        _arg(q_weight, f32, "q_weight", dev, D), _arg(k_weight, f32, "k_weight", dev, D), float(eps),
+        _arg(inv_freq, f32, "inv_freq", dev), rot, 1 if interleaved else 0, at_qo, ld_qo, ctype, bs, n_blocks, *at)
+    _check("sd_cache_append", code)
+    return dict(q=qo)
+
+
+@_on_device
+def sd_cache_read(row_slot, cache, out=None, dtype=torch.bfloat16, *, stream=None):
+    """Keys and values at slots of a paged cache as rows [rows][n_kv][D], in
+    bf16 or fp32 (out's type where given).  row_slot [rows] int64 (outside the
+    cache: the row is left as it is, undefined in new tensors), cache as for
+    sd_cache_append.  Returns a dict of device tensors: k, v."""
+    dev, device = row_slot.get_device(), row_slot.device
+    ctype, n_blocks, n_kv, bs, D, at = _cache_args(cache, dev)
+    n, o = row_slot.numel(), out or {}
+    if o:
+        dtype = next(iter(o.values())).dtype
+    make = lambda key: o[key] if key in o else torch.empty((n, n_kv, D), dtype=dtype, device=device)  # noqa: E731
+    ko, vo = make("k"), make("v")
+    at_k, ld_k = _heads(ko, dtype, "out k", dev, (n, n_kv, D))
+    at_v, ld_v = _heads(vo, dtype, "out v", dev, (n, n_kv, D))
+    _fits("sd_cache_read", n | n_kv | D | n_blocks | bs)
+    code = lib().sd_cache_read(
+        _raw_stream(dev), n, D, _arg(row_slot, torch.int64, "row_slot", dev), ctype, n_kv, bs, n_blocks, *at,
+        _row_type(ko, "out"), at_k, ld_k, at_v, ld_v)
+    _check("sd_cache_read", code)
+    return dict(k=ko, v=vo)

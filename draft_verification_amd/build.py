@@ -11,7 +11,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsdv.so")
 SOURCES = ["abi.hip", "schedule.hip", "row_partials.hip", "verify.hip", "markov.hip", "lightspec.hip",
-           "uniforms.hip", "shape.hip", "slots.hip"]
+           "uniforms.hip", "shape.hip", "slots.hip", "heads.hip"]
 PROBE_LIB = os.path.join(PKG, "libsdv_probe.so")
 PROBE_SOURCES = ["probe.hip"]
 

@@ -14,7 +14,8 @@
  * (the uniforms behind the random decisions), sd_slot_reserve and
  * sd_slot_commit (the verify batch's rows and paged cache slots),
  * sd_logit_shape and sd_token_counts (penalties, biases and grammar masks on
- * the target rows, and the token counts behind them).
+ * the target rows, and the token counts behind them), and what a layer of the
+ * target does with those slots: sd_qk_rope, sd_cache_append, sd_cache_read.
  *
  * Sources, by page and section:
  *   [DS]  "DSpark: Confidence-Scheduled Speculative Decoding with
@@ -54,8 +55,8 @@
  *   - bf16 data is passed as raw 16-bit patterns (uint16_t).
  *   - What a call writes (outputs, state, workspace) overlaps none of its other
  *     arguments, unless its text names them; sd_logit_shape, sd_token_counts,
- *     sd_slot_reserve and sd_slot_commit return SD_EINVAL where it does, by the
- *     sizes given.
+ *     sd_slot_reserve, sd_slot_commit, sd_qk_rope and the sd_cache_* calls
+ *     return SD_EINVAL where it does, by the sizes given.
  */
 #ifndef SDV_H
 #define SDV_H
@@ -81,6 +82,10 @@ extern "C" {
 #define SD_DTYPE_F32   0
 #define SD_DTYPE_BF16  1
 
+/* what a paged cache holds */
+#define SD_CACHE_BF16  0
+#define SD_CACHE_FP4   1
+
 /* sd_verify options */
 #define SD_VERIFY_STOP_AT_REJECTION 1
 
@@ -103,6 +108,7 @@ extern "C" {
 #define SD_MAX_GAMMA           255     /* draft positions per request */
 #define SD_MAX_SCHED_SLOTS     16384   /* R * gamma_max for sd_schedule */
 #define SD_MAX_VOCAB           (1 << 24)
+#define SD_MAX_HEADS           1024    /* heads of queries, or of keys */
 
 /* ABI version of the loaded library (SDV_ABI_VERSION at build time). */
 int sd_abi_version(void);
@@ -593,6 +599,76 @@ int sd_slot_commit(hipStream_t stream, int R, int q_max, int block_size, int max
                    int32_t* free_list, const int32_t* free_count, int32_t* status,
                    int64_t* seq_len_out, int32_t* x0_out, int32_t* n_new, int32_t* free_count_out,
                    void* workspace, size_t workspace_bytes);
+
+/*
+ * sd_qk_rope - norms of the heads of queries and keys, and their rotation by
+ * the row's position, in one pass (the target's layers on a verify batch's
+ * rows, sd_slot_reserve's row_pos; a drafter's layers, which have no paged
+ * cache).  A head x of D channels becomes
+ *     y = x / sqrt(mean(x^2) + eps) * w          (where its weights w are given)
+ * and of its first rot_dim channels each pair (a, b) becomes
+ *     (a cos t - b sin t, b cos t + a sin t),  t = pos[row] * inv_freq[i]
+ * pair i being channels (i, i + rot_dim/2), or (2i, 2i + 1) where interleaved
+ * is 1; the others stay.  t in fp64, the rest in fp32, rounded once.
+ *   n_rows >= 0; D % 8 == 0, D <= 256; rot_dim % 8 == 0, 0 <= rot_dim <= D;
+ *   dtype of q, k, q_out and k_out: SD_DTYPE_F32 or SD_DTYPE_BF16
+ *   q, k     rows of n_q and n_kv heads of D channels (either may be 0), ld
+ *            elements apart (ld % 8 == 0, such as parts of one projection's
+ *            rows), 16-byte aligned
+ *   pos      [n_rows] int32; a row with pos < 0 is no request's and is left
+ *            out (its outputs stay as they are).  May be NULL with rot_dim = 0
+ *   q_weight, k_weight  [D] fp32 or NULL: no norm.  eps >= 0, finite
+ *   inv_freq [rot_dim / 2] fp32: radians per position, however the model
+ *            scales them.  Weights and frequencies 16-byte aligned
+ *   q_out, k_out  may be q and k (with the same ld): in place
+ */
+int sd_qk_rope(hipStream_t stream, int n_rows, int D, int dtype, const void* q, int n_q, long long ld_q,
+               const void* k, int n_kv, long long ld_k, const int32_t* pos, const float* q_weight,
+               const float* k_weight, float eps, const float* inv_freq, int rot_dim, int interleaved,
+               void* q_out, long long ld_q_out, void* k_out, long long ld_k_out);
+
+/*
+ * A paged cache: keys and values of one layer, [n_blocks][n_kv][block_size][D]
+ * each, 16-byte aligned.  Row e of a step belongs at row_slot[e] =
+ * block * block_size + offset (sd_slot_reserve's).
+ *   SD_CACHE_BF16  bf16; k_scale and v_scale are not used
+ *   SD_CACHE_FP4   4 bits: [n_blocks][n_kv][block_size][D / 2] bytes, the
+ *                  even channel in a byte's low half: a sign bit over three
+ *                  bits for 0, .5, 1, 1.5, 2, 3, 4, 6 (e2m1); and
+ *                  k_scale, v_scale [n_blocks][n_kv][block_size][D / 32]:
+ *                  the values of 32 channels are 2^(byte - 127) times those.
+ *                  D % 32 == 0.  Written with the smallest scale (of at least
+ *                  2^-126) for which the group's largest magnitude is at most
+ *                  7, each channel at the nearest level, ties to the even
+ *                  code.  A group that is not finite gets byte 255: it reads
+ *                  as NaN.
+ *
+ * sd_cache_append - keys and values of a step's rows into their slots, the
+ * keys normed and rotated on the way as by sd_qk_rope, the values as they are;
+ * with queries (n_q > 0) these go to q_out as by sd_qk_rope, in the same
+ * launch.  k is rounded once, from fp32 to what the cache holds.
+ *   k, v     rows of n_kv heads; q, q_out, row_pos, weights, eps, inv_freq,
+ *            rot_dim, interleaved: sd_qk_rope's
+ *   row_slot [n_rows] int64.  A row whose slot is outside the cache (-1 for
+ *            rows without one) stores neither keys nor values; one with
+ *            row_pos < 0 stores nothing.  The other slots are distinct (of
+ *            rows that share one, the slot holds a mixture)
+ *   n_blocks * block_size at most 2^40
+ *
+ * sd_cache_read - the way back: the keys and values at row_slot as rows of
+ * n_kv heads, in bf16 (exact) or fp32; rows whose slot is outside the cache
+ * are left as they are.  Slots may repeat.
+ */
+int sd_cache_append(hipStream_t stream, int n_rows, int D, int dtype, const void* q, int n_q,
+                    long long ld_q, const void* k, long long ld_k, const void* v, long long ld_v, int n_kv,
+                    const int32_t* row_pos, const int64_t* row_slot, const float* q_weight,
+                    const float* k_weight, float eps, const float* inv_freq, int rot_dim, int interleaved,
+                    void* q_out, long long ld_q_out, int cache_type, int block_size, int n_blocks,
+                    void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale);
+int sd_cache_read(hipStream_t stream, int n_rows, int D, const int64_t* row_slot, int cache_type, int n_kv,
+                  int block_size, int n_blocks, const void* k_cache, const void* v_cache,
+                  const uint8_t* k_scale, const uint8_t* v_scale, int dtype, void* k_out, long long ld_k,
+                  void* v_out, long long ld_v);
 
 #ifdef __cplusplus
 }
