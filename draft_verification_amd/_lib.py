@@ -53,6 +53,7 @@ EXPORTS = (
     "sd_logit_shape", "sd_token_counts", "sd_slot_reserve_workspace_size", "sd_slot_reserve",
     "sd_slot_commit_workspace_size", "sd_slot_commit",
     "sd_qk_rope", "sd_cache_append", "sd_cache_read",
+    "sd_attn_workspace_size", "sd_attn_plan", "sd_cache_attn",
 )
 
 
@@ -136,6 +137,13 @@ def lib():
                                   _L, _I, _I, _I, _P, _P, _P, _P]
     L.sd_cache_read.restype = _I
     L.sd_cache_read.argtypes = [_P, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _L, _P, _L]
+    L.sd_attn_workspace_size.restype = _SZ
+    L.sd_attn_workspace_size.argtypes = [_I, _I, _I, _I, _I]
+    L.sd_attn_plan.restype = _I
+    L.sd_attn_plan.argtypes = [_P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P, _P, _SZ]
+    L.sd_cache_attn.restype = _I
+    L.sd_cache_attn.argtypes = [_P, _I, _I, _I, _I, _I, _I, _P, _L, _I, _I, _I, _P, _P, _P, _P, _P, _I, _F, _P, _L, _P,
+                                _P, _P, _SZ]
     _lib = L
     return L
 
@@ -877,3 +885,71 @@ def sd_cache_read(row_slot, cache, out=None, dtype=torch.bfloat16, *, stream=Non
         _row_type(ko, "out"), at_k, ld_k, at_v, ld_v)
     _check("sd_cache_read", code)
     return dict(k=ko, v=vo)
+
+
+def sd_attn_workspace_size(R, q_max, n_q, n_kv, D):
+    return lib().sd_attn_workspace_size(R, q_max, n_q, n_kv, D)
+
+
+@_on_device
+def sd_attn_plan(row0, ell, ctx_len, q_max, n_q, cache, causal=True, window=0, out=None, workspace=None, *,
+                 stream=None):
+    """Cut a step's attention into equal parts, once for all its layers.  row0,
+    ell, ctx_len [R] int32 as sd_slot_reserve leaves them, q_max its bound on
+    a request's rows, n_q query heads; cache: one layer's, for its sizes.
+    causal: a row sees the tokens up to its own, else all of its request's;
+    window > 0: only the last so many up to its own.  Returns a dict that
+    sd_cache_attn takes: workspace and status (device tensors) and the sizes
+    they are for."""
+    dev, device = row0.get_device(), row0.device
+    R = row0.numel()
+    ctype, _, n_kv, _, D, _ = _cache_args(cache, dev)
+    q_max, n_q, window = int(q_max), int(n_q), int(window)
+    _fits("sd_attn_plan", R | q_max | n_q | n_kv | D | window)
+    status = out["status"] if out and "status" in out else torch.empty(R, dtype=torch.int32, device=device)
+    ws = workspace if workspace is not None else _workspace(sd_attn_workspace_size(R, q_max, n_q, n_kv, D), device)
+    i32 = torch.int32
+    code = lib().sd_attn_plan(
+        _raw_stream(dev), R, q_max, n_q, n_kv, D, ctype, _arg(row0, i32, "row0", dev), _arg(ell, i32, "ell", dev, R),
+        _arg(ctx_len, i32, "ctx_len", dev, R), 1 if causal else 0, window, _arg(status, i32, "status", dev, R),
+        _arg(ws, torch.uint8, "workspace", dev), ws.numel())
+    _check("sd_attn_plan", code)
+    return dict(workspace=ws, status=status, R=R, q_max=q_max, n_q=n_q, n_kv=n_kv, D=D)
+
+
+@_on_device
+def sd_cache_attn(q, cache, block_table, plan, scale=None, lse=False, out=None, *, stream=None):
+    """Attention of a step's rows over a paged cache.  q [rows][n_q][D] bf16,
+    each row's heads together; cache as for sd_cache_append; block_table
+    [R][max_blocks] int32; plan: sd_attn_plan's for this step.  scale: 1 /
+    sqrt(D) if None.  lse: also return the log of each softmax's sum (or give
+    out["lse"], [rows][n_q] fp32).  Rows of no request are left as they are,
+    undefined in new tensors.  Returns a dict of device tensors: out, lse (or
+    None), status (the plan's, OR-ed into)."""
+    dev = q.get_device()
+    if q.dim() != 3:
+        raise ValueError("q must be [rows][n_q][D]")
+    n, n_q, D = q.shape
+    bf = torch.bfloat16
+    at_q, ld_q = _heads(q, bf, "q", dev)
+    ctype, n_blocks, n_kv, bs, c_D, at = _cache_args(cache, dev)
+    if (n_q, n_kv, D, D) != (plan["n_q"], plan["n_kv"], plan["D"], c_D):
+        raise ValueError(f"the plan is for {plan['n_q']} and {plan['n_kv']} heads of {plan['D']} channels, got "
+                         f"{n_q} and {n_kv} of {D} and {c_D}")
+    R = plan["R"]
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError(f"block_table must be [R][max_blocks] with R = {R}")
+    mb = block_table.shape[1]
+    o = out or {}
+    dst = o["out"] if "out" in o else torch.empty(q.shape, dtype=bf, device=q.device)
+    at_out, ld_out = _heads(dst, bf, "out", dev, q.shape)
+    z = o["lse"] if "lse" in o else torch.empty((n, n_q), dtype=torch.float32, device=q.device) if lse else None
+    _fits("sd_cache_attn", n | n_q | n_blocks | bs | mb)
+    ws = plan["workspace"]
+    code = lib().sd_cache_attn(
+        _raw_stream(dev), R, plan["q_max"], n_q, n_kv, D, n, at_q, ld_q, ctype, bs, n_blocks, *at,
+        _arg(block_table, torch.int32, "block_table", dev), mb, float(D ** -0.5 if scale is None else scale), at_out,
+        ld_out, _arg(z, torch.float32, "lse", dev, n * n_q), _arg(plan["status"], torch.int32, "status", dev, R),
+        _arg(ws, torch.uint8, "workspace", dev), ws.numel())
+    _check("sd_cache_attn", code)
+    return dict(out=dst, lse=z, status=plan["status"])

@@ -5,13 +5,15 @@ is not part of the library's interface)."""
 import os
 import shutil
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsdv.so")
 SOURCES = ["abi.hip", "schedule.hip", "row_partials.hip", "verify.hip", "markov.hip", "lightspec.hip",
-           "uniforms.hip", "shape.hip", "slots.hip", "heads.hip"]
+           "uniforms.hip", "shape.hip", "slots.hip", "heads.hip", "attend.hip", "attend_bf16.hip", "attend_fp4.hip"]
 PROBE_LIB = os.path.join(PKG, "libsdv_probe.so")
 PROBE_SOURCES = ["probe.hip"]
 
@@ -20,7 +22,6 @@ HIPCC_FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-Wall",
     # Packed FP32 instructions stay disabled: the compiler would otherwise
     # form v_pk_* fp32 ops from plain float code.
@@ -36,18 +37,25 @@ def hipcc() -> str:
     return path
 
 
-def _compile(sources, out, verbose):
-    srcs = [os.path.join(CSRC, s) for s in sources]
-    tmp = out + ".tmp"
-    cmd = [hipcc()] + HIPCC_FLAGS + ["-o", tmp] + srcs
-    res = subprocess.run(cmd, capture_output=True, text=True)
+def _hipcc(args, verbose):
+    res = subprocess.run([hipcc()] + HIPCC_FLAGS + args, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("hipcc failed:\n" + res.stdout + res.stderr)
     if verbose:
         err = "\n".join(l for l in res.stderr.splitlines() if "packed-fp32-ops" not in l)
         if err.strip():
             print(err)
-    os.replace(tmp, out)
+
+
+def _compile(sources, out, verbose):
+    """Each source by itself, a few at a time, then one link."""
+    with tempfile.TemporaryDirectory() as tmp:
+        objs = [os.path.join(tmp, s + ".o") for s in sources]
+        with ThreadPoolExecutor(min(len(sources), os.cpu_count() or 1, 8)) as pool:
+            list(pool.map(lambda so: _hipcc(["-c", os.path.join(CSRC, so[0]), "-o", so[1]], verbose),
+                          zip(sources, objs)))
+        _hipcc(["-shared", "-o", out + ".tmp"] + objs, verbose)
+    os.replace(out + ".tmp", out)
 
 
 def build(verbose: bool = False) -> str:

@@ -1,0 +1,123 @@
+// Attention of a step's rows over a paged cache: the plan of a step and what
+// its kernels share.
+//
+// Queries of one key head - the rows of a request times the heads of a group,
+// row by row - are taken M at a time: a tile.  A tile's tokens are taken TT at
+// a time: units, whose keys and values pass through LDS once for all M
+// queries.  Requests differ in length by orders of magnitude, and only the
+// device knows them, so the units of all tiles, head after head, are cut into
+// equal runs, one per workgroup: a run holds the end of one tile, whole tiles,
+// and the beginning of another.  Whole tiles are finished where they are
+// computed; the parts of a cut one go to the workspace, and a second launch
+// joins them, in their order.
+#pragma once
+
+#include "cache_common.h"
+#include "sdv_host.h"
+
+namespace sdv {
+
+constexpr int kAttnThreads = 256;
+constexpr uint32_t kPlanMark = 0x5D9A7713u;
+
+// What a plan was made for; the attention call has to say the same.
+struct PlanShape {
+  uint32_t mark;
+  int R, q_max, n_q, n_kv, D, type;
+};
+
+struct PlanHead {
+  PlanShape shape;
+  int causal, window;
+  int n_tiles;
+  int runs;          // workgroups with units
+  long long per_head, total, quota;   // units: of one head, of all, per workgroup
+};
+
+struct Tile {
+  int req, q0;       // request; first query, row * group + head of the group
+  int u0, units;     // first unit of tokens and how many
+  int queries;       // of the request
+  int ctx, row0, n;  // tokens, first row and rows of the request
+};
+
+struct Start {
+  int head, tile, off;   // where a workgroup's run begins; off: units into the tile
+};
+
+// How a call is cut up, from what the host knows.
+struct Cut {
+  int M, TT, W;            // queries per tile, tokens per unit, workgroups
+  long long max_tiles;
+  size_t tiles, sums, starts, ml, part, bytes;   // offsets in the workspace
+};
+
+// Queries per tile: as few as hold those of a request's largest step (a
+// workgroup multiplies all M columns, used or not), and at most what the
+// registers hold beside the output's M x D sums.
+inline int attn_queries(int q_max, int group, int D) {
+  const long long n = (long long)q_max * group;
+  if (D > 128) return n <= 32 ? 32 : 64;
+  return n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : 128;
+}
+inline int attn_unit(int D) { return D <= 128 ? 64 : 32; }
+
+inline Cut attn_cut(int R, int q_max, int n_q, int n_kv, int D) {
+  Cut c;
+  c.M = attn_queries(q_max, n_q / n_kv, D);
+  c.TT = attn_unit(D);
+  c.W = 512;               // two workgroups with 64 KB of LDS on each of 256 CUs
+  c.max_tiles = (long long)R * (((long long)q_max * (n_q / n_kv) + c.M - 1) / c.M);
+  size_t at = 256;
+  auto take = [&](size_t n) {
+    const size_t p = at;
+    at = sdv_align256(at + n);
+    return p;
+  };
+  c.tiles = take(sizeof(Tile) * (size_t)c.max_tiles);
+  c.sums = take(8 * ((size_t)c.max_tiles + 1));
+  c.starts = take(sizeof(Start) * ((size_t)c.W + 1));
+  c.ml = take(8 * 2 * (size_t)c.W * c.M);
+  c.part = take(4 * 2 * (size_t)c.W * c.M * D);
+  c.bytes = at;
+  return c;
+}
+
+struct AttnArgs {
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  long long ld_q, ld_out;
+  const int32_t* table;
+  int32_t* status;
+  Cache cache;
+  PlanShape shape;
+  int max_blocks, n_rows;
+  const PlanHead* head;
+  const Tile* tiles;
+  const Start* starts;
+  float2* ml;        // [2 W][M] running maximum and sum of a part
+  float* part;       // [2 W][M][D] its values, not divided yet
+  float scale2;      // scale * log2(e)
+  uint32_t block_tokens;   // n_kv * bs
+  uint32_t bs_mul;   // token / bs = token * bs_mul >> bs_shift
+  int bs_shift;
+  int group;
+  int n_q;
+};
+
+SDV_DEV bool same_shape(const PlanShape& x, const PlanShape& y) {
+  return x.mark == y.mark && x.R == y.R && x.q_max == y.q_max && x.n_q == y.n_q && x.n_kv == y.n_kv && x.D == y.D &&
+         x.type == y.type;
+}
+
+// The plan knows neither the table's width nor the rows of the buffers.
+SDV_DEV bool in_range(const AttnArgs& a, const Tile& t) {
+  return t.row0 <= a.n_rows - t.n && t.ctx <= (int64_t)a.max_blocks * a.cache.bs;
+}
+
+// One launch of the kernel for D, M and the cache's type.
+int attend_bf16(hipStream_t stream, int M, int W, const AttnArgs& a);
+int attend_fp4(hipStream_t stream, int M, int W, const AttnArgs& a);
+
+}  // namespace sdv

@@ -15,7 +15,8 @@
  * sd_slot_commit (the verify batch's rows and paged cache slots),
  * sd_logit_shape and sd_token_counts (penalties, biases and grammar masks on
  * the target rows, and the token counts behind them), and what a layer of the
- * target does with those slots: sd_qk_rope, sd_cache_append, sd_cache_read.
+ * target does with those slots: sd_qk_rope, sd_cache_append, sd_cache_read,
+ * sd_attn_plan and sd_cache_attn.
  *
  * Sources, by page and section:
  *   [DS]  "DSpark: Confidence-Scheduled Speculative Decoding with
@@ -55,8 +56,8 @@
  *   - bf16 data is passed as raw 16-bit patterns (uint16_t).
  *   - What a call writes (outputs, state, workspace) overlaps none of its other
  *     arguments, unless its text names them; sd_logit_shape, sd_token_counts,
- *     sd_slot_reserve, sd_slot_commit, sd_qk_rope and the sd_cache_* calls
- *     return SD_EINVAL where it does, by the sizes given.
+ *     sd_slot_reserve, sd_slot_commit, sd_qk_rope, sd_attn_plan and the
+ *     sd_cache_* calls return SD_EINVAL where it does, by the sizes given.
  */
 #ifndef SDV_H
 #define SDV_H
@@ -669,6 +670,66 @@ int sd_cache_read(hipStream_t stream, int n_rows, int D, const int64_t* row_slot
                   int block_size, int n_blocks, const void* k_cache, const void* v_cache,
                   const uint8_t* k_scale, const uint8_t* v_scale, int dtype, void* k_out, long long ld_k,
                   void* v_out, long long ld_v);
+
+/*
+ * Attention of a step's rows over a paged cache [SD 1.1: the target scores all
+ * drafts in one pass; LS: requests of very different lengths].
+ *
+ * Request r has n = min(ell[r] + 1, q_max) rows (none where ell[r] < 0) at
+ * row0[r].., and ctx_len[r] tokens in the cache, its rows' own included: row i
+ * stands at position ctx_len[r] - n + i.  (sd_slot_reserve's ell_out, row0 and
+ * ctx_len.)  Query head h reads key head h / (n_q / n_kv).  With
+ * S_t = scale * q . k_t over the tokens t that the row sees,
+ *     out = sum_t softmax(S)_t v_t,   lse = log sum_t exp(S_t).
+ * A row sees t <= its position where causal is 1, else all ctx_len[r] tokens
+ * (a drafter's block that is scored at once); with window > 0 of those only
+ * t > position - window.  A row that sees nothing, or whose scores are all
+ * -inf, gives zeros and lse = -inf.  What a row does not see does not touch
+ * it, whatever the cache holds there.
+ *
+ * sd_attn_plan - once per step: cuts the step's work into equal runs for the
+ * chip's workgroups, into the workspace that the step's sd_cache_attn calls
+ * (one per layer) are given.  Another mask needs a plan of its own.
+ *   R >= 0; q_max >= 1 (rows of a request, as in sd_slot_reserve); n_q a
+ *   multiple of n_kv; D 64, 96, 128, 192 or 256; R * q_max * n_q / n_kv below
+ *   2^31 - 257; cache_type SD_CACHE_BF16 or SD_CACHE_FP4
+ *   status     [R] int32 out: BAD_INPUT where ctx_len is below the request's
+ *              rows or past 2^31 - 257, or row0 is negative: its rows are
+ *              left as they are
+ *   workspace  sd_attn_workspace_size(R, q_max, n_q, n_kv, D) bytes, 256-byte
+ *              aligned
+ *
+ * sd_cache_attn - one layer's attention with a plan.  R, q_max, n_q, n_kv, D,
+ * cache_type as the plan's (with others nothing is written).
+ *   q, out       [n_rows] rows of n_q heads, bf16, ld elements apart (ld % 8
+ *                == 0), 16-byte aligned; rows of no request are left as they
+ *                are in out
+ *   the cache    as sd_cache_append writes it, n_blocks >= 1
+ *   block_table  [R][max_blocks] int32, block_size * max_blocks below
+ *                2^31 - 257.  Entries past ctx_len are not used
+ *   scale        > 0, finite
+ *   lse          [n_rows][n_q] fp32 or NULL
+ *   status       [R] int32, OR-ed into (give it the plan's): BAD_INPUT where
+ *                the request's rows or tokens are past the row buffers or its
+ *                table's row (left as they are), or a block is outside the
+ *                pool (its tokens are not seen).  Rows without slots
+ *                (sd_slot_reserve's BAD_INPUT) are computed like others
+ *   workspace    the plan's, unchanged but by these calls; calls that may run
+ *                at the same time need workspaces and plans of their own
+ * Scores, weights' sums and outputs are held in fp32; the weights are rounded
+ * to bf16 for the product with the values, and out once more.  Results do not
+ * depend on the order in which workgroups run, but a request's last bits do on
+ * how the step is cut, so on the other requests.
+ */
+size_t sd_attn_workspace_size(int R, int q_max, int n_q, int n_kv, int D);
+int sd_attn_plan(hipStream_t stream, int R, int q_max, int n_q, int n_kv, int D, int cache_type,
+                 const int32_t* row0, const int32_t* ell, const int32_t* ctx_len, int causal, int window,
+                 int32_t* status, void* workspace, size_t workspace_bytes);
+int sd_cache_attn(hipStream_t stream, int R, int q_max, int n_q, int n_kv, int D, int n_rows,
+                  const uint16_t* q, long long ld_q, int cache_type, int block_size, int n_blocks,
+                  const void* k_cache, const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                  const int32_t* block_table, int max_blocks, float scale, uint16_t* out, long long ld_out,
+                  float* lse, int32_t* status, void* workspace, size_t workspace_bytes);
 
 #ifdef __cplusplus
 }
