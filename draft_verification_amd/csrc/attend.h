@@ -30,8 +30,9 @@ struct PlanHead {
   PlanShape shape;
   int causal, window;
   int n_tiles;
-  int runs;          // workgroups with units
-  long long per_head, total, quota;   // units: of one head, of all, per workgroup
+  int n_cuts;
+  int slices;                // of a cut tile's parts, joined side by side
+  long long total, quota;    // units: of all heads, per workgroup
 };
 
 struct Tile {
@@ -41,15 +42,24 @@ struct Tile {
   int ctx, row0, n;  // tokens, first row and rows of the request
 };
 
+// Where a workgroup's run begins: off units into tile `index`, a copy of which
+// is here, so that a run begins with one read.
 struct Start {
-  int head, tile, off;   // where a workgroup's run begins; off: units into the tile
+  Tile tile;
+  int head, index, off, pad;
+};
+
+// A tile in parts: runs first .. last have one each.
+struct CutTile {
+  Tile tile;
+  int head, first, last, pad;
 };
 
 // How a call is cut up, from what the host knows.
 struct Cut {
   int M, TT, W;            // queries per tile, tokens per unit, workgroups
   long long max_tiles;
-  size_t tiles, sums, starts, ml, part, bytes;   // offsets in the workspace
+  size_t tiles, sums, starts, cuts, ml, part, bytes;   // offsets in the workspace
 };
 
 // Queries per tile: as few as hold those of a request's largest step (a
@@ -60,12 +70,20 @@ inline int attn_queries(int q_max, int group, int D) {
   if (D > 128) return n <= 32 ? 32 : 64;
   return n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : 128;
 }
-inline int attn_unit(int D) { return D <= 128 ? 64 : 32; }
+// Tokens per unit.
+constexpr int attn_unit(int D, int M, bool fp4) {
+  return fp4 ? (D <= 128 && M < 128 ? 128 : 64) : D <= 128 ? 64 : 32;
+}
+// Neighbouring tokens that a wave loads with one address where they lie in one
+// block: all of its quarter of a unit, or, in 4 bits, those of one load; 0: never.
+constexpr int attn_span(int D, int M, bool fp4) {
+  return !fp4 ? attn_unit(D, M, fp4) / 4 : 64 % (D / 32) == 0 ? 64 / (D / 32) : 0;
+}
 
-inline Cut attn_cut(int R, int q_max, int n_q, int n_kv, int D) {
+inline Cut attn_cut(int R, int q_max, int n_q, int n_kv, int D, int type) {
   Cut c;
   c.M = attn_queries(q_max, n_q / n_kv, D);
-  c.TT = attn_unit(D);
+  c.TT = attn_unit(D, c.M, type == SD_CACHE_FP4);
   c.W = 512;               // two workgroups with 64 KB of LDS on each of 256 CUs
   c.max_tiles = (long long)R * (((long long)q_max * (n_q / n_kv) + c.M - 1) / c.M);
   size_t at = 256;
@@ -77,6 +95,7 @@ inline Cut attn_cut(int R, int q_max, int n_q, int n_kv, int D) {
   c.tiles = take(sizeof(Tile) * (size_t)c.max_tiles);
   c.sums = take(8 * ((size_t)c.max_tiles + 1));
   c.starts = take(sizeof(Start) * ((size_t)c.W + 1));
+  c.cuts = take(sizeof(CutTile) * (size_t)c.W);
   c.ml = take(8 * 2 * (size_t)c.W * c.M);
   c.part = take(4 * 2 * (size_t)c.W * c.M * D);
   c.bytes = at;
@@ -96,12 +115,15 @@ struct AttnArgs {
   const PlanHead* head;
   const Tile* tiles;
   const Start* starts;
+  const CutTile* cuts;
   float2* ml;        // [2 W][M] running maximum and sum of a part
   float* part;       // [2 W][M][D] its values, not divided yet
   float scale2;      // scale * log2(e)
   uint32_t block_tokens;   // n_kv * bs
   uint32_t bs_mul;   // token / bs = token * bs_mul >> bs_shift
   int bs_shift;
+  int spans;         // tokens that are loaded together lie in one block
+  int once;          // a request is one tile: what is loaded is not needed again
   int group;
   int n_q;
 };

@@ -21,6 +21,7 @@ struct PlanArgs {
   Tile* tiles;
   long long* sums;
   Start* starts;
+  CutTile* cuts;
   PlanShape shape;
   int causal, window, M, TT, W, group;
 };
@@ -92,74 +93,137 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(PlanArgs a) {
   long long quota = (all + a.W - 1) / a.W;
   if (quota < kMinQuota) quota = kMinQuota;
   __syncthreads();
-  for (int w = threadIdx.x; w <= a.W; w += blockDim.x) {
-    const long long at = w * quota;
-    Start s = {0, 0, 0};
-    if (at < all) {
-      s.head = (int)(at / units);
-      const long long rest = at - s.head * units;
-      long long lo = 0, hi = n_tiles;   // sums[lo] <= rest < sums[hi]
-      while (hi - lo > 1) {
-        const long long mid = (lo + hi) >> 1;
-        if (a.sums[mid] <= rest) lo = mid;
-        else hi = mid;
-      }
-      s.tile = (int)lo;
-      s.off = (int)(rest - a.sums[lo]);
+  // One thread per run (no more than threads): where it begins, and whether
+  // the tile at its end is cut there and began in it.
+  const int w = threadIdx.x;
+  Start s = {};
+  auto start_of = [&](int run) {
+    const long long at = run * quota;
+    Start x = {};
+    if (run >= a.W || at >= all) return x;
+    x.head = (int)(at / units);
+    const long long rest = at - x.head * units;
+    long long lo = 0, hi = n_tiles;   // sums[lo] <= rest < sums[hi]
+    while (hi - lo > 1) {
+      const long long mid = (lo + hi) >> 1;
+      if (a.sums[mid] <= rest) lo = mid;
+      else hi = mid;
     }
-    a.starts[w] = s;
+    x.index = (int)lo;
+    x.off = (int)(rest - a.sums[lo]);
+    x.tile = a.tiles[lo];
+    return x;
+  };
+  s = start_of(w);
+  if (w < a.W) a.starts[w] = s;
+  const Start next = start_of(w + 1);
+  const bool cut = next.off > 0 && next.off <= quota;
+  const long long at = block_scan(cut ? 1 : 0, part, &total);
+  const long long n_cuts = total;
+  int last = 0;
+  if (cut) {
+    last = (int)(((w + 1) * quota - next.off + next.tile.units - 1) / quota);
+    a.cuts[at] = CutTile{next.tile, next.head, w, last, 0};
   }
+  block_scan(cut ? last - w + 1 : 0, part, &total);
   if (threadIdx.x == 0) {
     PlanHead h = {};
     h.shape = a.shape;
     h.causal = a.causal;
     h.window = a.window;
     h.n_tiles = (int)n_tiles;
-    h.per_head = units;
+    h.n_cuts = (int)n_cuts;
+    // eight parts or more to a slice
+    h.slices = 1;
+    while (h.slices < 8 && total >= 16 * h.slices * n_cuts) h.slices *= 2;
     h.total = all;
     h.quota = quota;
     *a.head = h;
   }
 }
 
-// Joins the parts of the tile that run w began and did not finish; D / 4
-// threads to a query.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinGrid = 2048;
+constexpr int kJoinQueries = 4;   // of a thread, whose loads are on their way together
+
+// Joins the parts of cut tiles, in the order of the runs: D / 4 threads to a
+// query and a slice of its parts (every slices-th one), slices through LDS.
 template <int D>
-__global__ __launch_bounds__(256) void k_join(AttnArgs a, int M) {
-  constexpr int TQ = D / 4, QB = 256 / TQ;
+__global__ __launch_bounds__(kJoinThreads) void k_join(AttnArgs a, int M) {
+  constexpr int TQ = D / 4, QB = kJoinThreads / TQ, NQ = kJoinQueries;
+  __shared__ float4 so[NQ][kJoinThreads];
+  __shared__ float2 sml[NQ][kJoinThreads];
   const PlanHead& p = *a.head;
   if (!same_shape(p.shape, a.shape)) return;
-  const int w = blockIdx.x, q = blockIdx.y * QB + threadIdx.x / TQ, d = threadIdx.x % TQ * 4;
-  const long long quota = p.quota, end = (w + 1) * quota;
-  if (end >= p.total) return;
-  const Start s = a.starts[w + 1];
-  if (s.off == 0 || s.off > quota) return;   // no tile is cut here, or a run before began it
-  const Tile t = a.tiles[s.tile];
-  if (!in_range(a, t)) return;
-  const int qi = t.q0 + q;
-  if (threadIdx.x >= QB * TQ || q >= M || qi >= t.queries) return;
-  const int last = (int)((end - s.off + t.units - 1) / quota);   // the run that ends it
-  auto slot = [&](int k) { return (int64_t)(k == w ? 2 * w + 1 : 2 * k) * M + q; };
-  float top = -__builtin_huge_valf();
-  for (int k = w; k <= last; ++k) top = fmaxf(top, a.ml[slot(k)].x);
-  const float ref = top == -__builtin_huge_valf() ? 0.f : top;
-  float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = w; k <= last; ++k) {
-    const float2 ml = a.ml[slot(k)];
-    const float f = fast_exp2(ml.x - ref);
-    const float4 v = *(const float4*)(a.part + slot(k) * D + d);
-    l += ml.y * f;
-    o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
+  const int slices = p.slices <= QB ? p.slices : QB >= 8 ? 8 : 4;   // QB is 4 at least
+  const int per = QB / slices, jobs = (M + per * NQ - 1) / (per * NQ);
+  const int mine = threadIdx.x / TQ, d = threadIdx.x % TQ * 4, slice = mine / per;
+  for (long long job = blockIdx.x; job < (long long)p.n_cuts * jobs; job += gridDim.x) {
+    const CutTile c = a.cuts[job / jobs];
+    const Tile& t = c.tile;
+    if (!in_range(a, t)) continue;   // the same for all threads
+    const int q0 = (int)(job % jobs) * per * NQ + mine % per;   // and every per-th one behind it
+    float top[NQ], l[NQ] = {};
+    float4 o[NQ];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      top[i] = -__builtin_huge_valf();
+      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    auto add = [&](int i, float m, float sum, const float4& v) {
+      const float to = fmaxf(top[i], m), ref = to == -__builtin_huge_valf() ? 0.f : to;
+      const float f = fast_exp2(top[i] - ref), h = fast_exp2(m - ref);
+      top[i] = to;
+      l[i] = l[i] * f + sum * h;
+      o[i].x = o[i].x * f + v.x * h, o[i].y = o[i].y * f + v.y * h;
+      o[i].z = o[i].z * f + v.z * h, o[i].w = o[i].w * f + v.w * h;
+    };
+    if (slice < slices) {
+#pragma unroll 2
+      for (int k = c.first + slice; k <= c.last; k += slices) {
+        const int64_t slot = (int64_t)(k == c.first ? 2 * k + 1 : 2 * k) * M;
+        float2 ml[NQ];
+        float4 v[NQ];
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          const int q = q0 + i * per, at = q < M && t.q0 + q < t.queries ? q : 0;   // column 0 is always a query
+          ml[i] = a.ml[slot + at];
+          v[i] = *(const float4*)(a.part + (slot + at) * D + d);
+        }
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) add(i, ml[i].x, ml[i].y, v[i]);
+      }
+    }
+    if (slices > 1) {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        so[i][threadIdx.x] = o[i];
+        sml[i][threadIdx.x] = make_float2(top[i], l[i]);
+      }
+      __syncthreads();
+      if (slice == 0)
+        for (int k = 1; k < slices; ++k)
+#pragma unroll
+          for (int i = 0; i < NQ; ++i) {
+            const int from = threadIdx.x + k * per * TQ;
+            add(i, sml[i][from].x, sml[i][from].y, so[i][from]);
+          }
+      __syncthreads();
+    }
+    if (slice > 0) continue;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int q = q0 + i * per, qi = t.q0 + q;
+      if (q >= M || qi >= t.queries) continue;
+      const int row = qi / a.group, head = c.head * a.group + qi - row * a.group;
+      const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+      *(uint2*)(a.out + (int64_t)(t.row0 + row) * a.ld_out + (int64_t)head * D + d) =
+          make_uint2(pack_bf16(o[i].x * inv, o[i].y * inv), pack_bf16(o[i].z * inv, o[i].w * inv));
+      if (a.lse && d == 0)
+        a.lse[(int64_t)(t.row0 + row) * a.n_q + head] =
+            l[i] == 0.f ? -__builtin_huge_valf() : (top[i] + __log2f(l[i])) * 0.69314718055994531f;
+    }
   }
-  const int i = qi / a.group, head = s.head * a.group + qi - i * a.group;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  *(uint2*)(a.out + (int64_t)(t.row0 + i) * a.ld_out + (int64_t)head * D + d) =
-      make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-  if (a.lse && d == 0)
-    a.lse[(int64_t)(t.row0 + i) * a.n_q + head] =
-        l == 0.f ? -__builtin_huge_valf() : (top + __log2f(l)) * 0.69314718055994531f;
 }
 
 bool head_dim(int D) { return D == 64 || D == 96 || D == 128 || D == 192 || D == 256; }
@@ -179,7 +243,7 @@ bool off256(const void* p) { return ((uintptr_t)p & 255) != 0; }
 
 extern "C" size_t sd_attn_workspace_size(int R, int q_max, int n_q, int n_kv, int D) {
   if (check_shape(R, q_max, n_q, n_kv, D, SD_CACHE_BF16) != SD_OK) return 0;
-  return attn_cut(R, q_max, n_q, n_kv, D).bytes;
+  return attn_cut(R, q_max, n_q, n_kv, D, SD_CACHE_BF16).bytes;   // the same for both types
 }
 
 extern "C" int sd_attn_plan(hipStream_t stream, int R, int q_max, int n_q, int n_kv, int D, int cache_type,
@@ -190,7 +254,7 @@ extern "C" int sd_attn_plan(hipStream_t stream, int R, int q_max, int n_q, int n
   if ((causal != 0 && causal != 1) || window < 0) return SD_EINVAL;
   if (R == 0) return SD_OK;
   if (!row0 || !ell || !ctx_len || !status || !workspace || off256(workspace)) return SD_EINVAL;
-  const Cut c = attn_cut(R, q_max, n_q, n_kv, D);
+  const Cut c = attn_cut(R, q_max, n_q, n_kv, D, cache_type);
   if (workspace_bytes < c.bytes) return SD_ERANGE;
   const Span written[] = {span(status, 4ll * R), span(workspace, (long long)c.bytes)};
   const Span read[] = {span(row0, 4ll * R), span(ell, 4ll * R), span(ctx_len, 4ll * R)};
@@ -199,7 +263,7 @@ extern "C" int sd_attn_plan(hipStream_t stream, int R, int q_max, int n_q, int n
   PlanArgs a = {};
   a.row0 = row0, a.ell = ell, a.ctx = ctx_len, a.status = status;
   a.head = (PlanHead*)ws, a.tiles = (Tile*)(ws + c.tiles), a.sums = (long long*)(ws + c.sums);
-  a.starts = (Start*)(ws + c.starts);
+  a.starts = (Start*)(ws + c.starts), a.cuts = (CutTile*)(ws + c.cuts);
   a.shape = PlanShape{kPlanMark, R, q_max, n_q, n_kv, D, cache_type};
   a.causal = causal, a.window = window, a.M = c.M, a.TT = c.TT, a.W = c.W, a.group = n_q / n_kv;
   SDV_TRY_LAUNCH(launch(k_plan, dim3(1), dim3(kPlanThreads), 0, stream, a));
@@ -225,7 +289,7 @@ extern "C" int sd_cache_attn(hipStream_t stream, int R, int q_max, int n_q, int 
   if (cache_type == SD_CACHE_FP4 && (!k_scale || !v_scale)) return SD_EINVAL;
   if (off16(q) || off16(out) || off16(k_cache) || off16(v_cache) || off256(workspace)) return SD_EINVAL;
   if (ld_q < width || ld_q % 8 != 0 || ld_out < width || ld_out % 8 != 0) return SD_EINVAL;
-  const Cut c = attn_cut(R, q_max, n_q, n_kv, D);
+  const Cut c = attn_cut(R, q_max, n_q, n_kv, D, cache_type);
   if (workspace_bytes < c.bytes) return SD_ERANGE;
   const bool fp4 = cache_type == SD_CACHE_FP4;
   const long long tokens = (long long)n_blocks * block_size * n_kv;
@@ -243,6 +307,7 @@ extern "C" int sd_cache_attn(hipStream_t stream, int R, int q_max, int n_q, int 
   a.shape = PlanShape{kPlanMark, R, q_max, n_q, n_kv, D, cache_type};
   a.max_blocks = max_blocks, a.n_rows = n_rows;
   a.head = (const PlanHead*)ws, a.tiles = (const Tile*)(ws + c.tiles), a.starts = (const Start*)(ws + c.starts);
+  a.cuts = (const CutTile*)(ws + c.cuts);
   a.ml = (float2*)(ws + c.ml), a.part = (float*)(ws + c.part);
   a.scale2 = scale * kLog2e;
   // token * ceil(2^(31 + s) / bs) >> (31 + s), 2^s >= bs: exact below 2^31
@@ -251,15 +316,13 @@ extern "C" int sd_cache_attn(hipStream_t stream, int R, int q_max, int n_q, int 
   a.bs_mul = (uint32_t)(((1ull << (31 + s)) + block_size - 1) / block_size);
   a.bs_shift = 31 + s;
   a.group = n_q / n_kv, a.n_q = n_q, a.block_tokens = (uint32_t)(n_kv * block_size);
+  const int span = attn_span(D, c.M, fp4);
+  a.once = (long long)q_max * (n_q / n_kv) <= c.M;
+  a.spans = span > 0 && block_size % span == 0;
   const int done = fp4 ? attend_fp4(stream, c.M, c.W, a) : attend_bf16(stream, c.M, c.W, a);
   if (done != SD_OK) return done;
-#define SDV_JOIN(DD)                                                                                   \
-  case DD: {                                                                                           \
-    constexpr int kQueries = 256 / (DD / 4);                                                           \
-    const dim3 grid((unsigned)c.W, (unsigned)((c.M + kQueries - 1) / kQueries));                       \
-    SDV_TRY_LAUNCH(launch(k_join<DD>, grid, dim3(256), 0, stream, a, c.M));                            \
-    return SD_OK;                                                                                      \
-  }
+#define SDV_JOIN(DD) \
+  case DD: SDV_TRY_LAUNCH(launch(k_join<DD>, dim3(kJoinGrid), dim3(kJoinThreads), 0, stream, a, c.M)); return SD_OK;
   switch (D) {
     SDV_JOIN(64)
     SDV_JOIN(96)
