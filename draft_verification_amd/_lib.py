@@ -140,7 +140,7 @@ def lib():
     L.sd_attn_workspace_size.restype = _SZ
     L.sd_attn_workspace_size.argtypes = [_I, _I, _I, _I, _I]
     L.sd_attn_plan.restype = _I
-    L.sd_attn_plan.argtypes = [_P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P, _P, _SZ]
+    L.sd_attn_plan.argtypes = [_P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P, _P, _SZ]
     L.sd_cache_attn.restype = _I
     L.sd_cache_attn.argtypes = [_P, _I, _I, _I, _I, _I, _I, _P, _L, _I, _I, _I, _P, _P, _P, _P, _P, _I, _F, _P, _L, _P,
                                 _P, _P, _SZ]
@@ -903,14 +903,14 @@ def sd_attn_plan(row0, ell, ctx_len, q_max, n_q, cache, causal=True, window=0, o
     they are for."""
     dev, device = row0.get_device(), row0.device
     R = row0.numel()
-    ctype, _, n_kv, _, D, _ = _cache_args(cache, dev)
+    ctype, _, n_kv, bs, D, _ = _cache_args(cache, dev)
     q_max, n_q, window = int(q_max), int(n_q), int(window)
-    _fits("sd_attn_plan", R | q_max | n_q | n_kv | D | window)
+    _fits("sd_attn_plan", R | q_max | n_q | n_kv | D | bs | window)
     status = out["status"] if out and "status" in out else torch.empty(R, dtype=torch.int32, device=device)
     ws = workspace if workspace is not None else _workspace(sd_attn_workspace_size(R, q_max, n_q, n_kv, D), device)
     i32 = torch.int32
     code = lib().sd_attn_plan(
-        _raw_stream(dev), R, q_max, n_q, n_kv, D, ctype, _arg(row0, i32, "row0", dev), _arg(ell, i32, "ell", dev, R),
+        _raw_stream(dev), R, q_max, n_q, n_kv, D, ctype, bs, _arg(row0, i32, "row0", dev), _arg(ell, i32, "ell", dev, R),
         _arg(ctx_len, i32, "ctx_len", dev, R), 1 if causal else 0, window, _arg(status, i32, "status", dev, R),
         _arg(ws, torch.uint8, "workspace", dev), ws.numel())
     _check("sd_attn_plan", code)

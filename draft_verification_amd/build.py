@@ -13,7 +13,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsdv.so")
 SOURCES = ["abi.hip", "schedule.hip", "row_partials.hip", "verify.hip", "markov.hip", "lightspec.hip",
-           "uniforms.hip", "shape.hip", "slots.hip", "heads.hip", "attend.hip", "attend_bf16.hip", "attend_fp4.hip"]
+           "uniforms.hip", "shape.hip", "slots.hip", "heads.hip", "attend.hip", "attend_bf16.hip", "attend_fp4.hip",
+           "attend_direct.hip"]
 PROBE_LIB = os.path.join(PKG, "libsdv_probe.so")
 PROBE_SOURCES = ["probe.hip"]
 

@@ -12,6 +12,8 @@
 // joins them, in their order.
 #pragma once
 
+#include <initializer_list>
+
 #include "cache_common.h"
 #include "sdv_host.h"
 
@@ -23,7 +25,7 @@ constexpr uint32_t kPlanMark = 0x5D9A7713u;
 // What a plan was made for; the attention call has to say the same.
 struct PlanShape {
   uint32_t mark;
-  int R, q_max, n_q, n_kv, D, type;
+  int R, q_max, n_q, n_kv, D, type, bs;
 };
 
 struct PlanHead {
@@ -57,34 +59,45 @@ struct CutTile {
 
 // How a call is cut up, from what the host knows.
 struct Cut {
+  bool direct;
   int M, TT, W;            // queries per tile, tokens per unit, workgroups
   long long max_tiles;
   size_t tiles, sums, starts, cuts, ml, part, bytes;   // offsets in the workspace
 };
 
+// Whether a wave computes all queries of a tile of M (attend_direct.h): in 4
+// bits, where neighbouring channels of a lane share scales and 16 neighbouring
+// tokens a block, as long as the output's M x D sums fit its registers.
+constexpr bool attn_direct(int D, int M, bool fp4, int bs) {
+  return fp4 && bs % 16 == 0 && ((D == 64 && M <= 64) || (D == 128 && M <= 48) || (D == 256 && M <= 16));
+}
+
 // Queries per tile: as few as hold those of a request's largest step (a
 // workgroup multiplies all M columns, used or not), and at most what the
-// registers hold beside the output's M x D sums.
-inline int attn_queries(int q_max, int group, int D) {
+// registers hold beside the output's sums.
+inline int attn_queries(int q_max, int group, int D, bool fp4, int bs) {
   const long long n = (long long)q_max * group;
-  if (D > 128) return n <= 32 ? 32 : 64;
-  return n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : 128;
+  for (int M : {16, 32, 48})
+    if (n <= M && (attn_direct(D, M, fp4, bs) || M == 32 || (M == 16 && D <= 128))) return M;
+  return n <= 64 || D > 128 ? 64 : 128;
 }
 // Tokens per unit.
 constexpr int attn_unit(int D, int M, bool fp4) {
   return fp4 ? (D <= 128 && M < 128 ? 128 : 64) : D <= 128 ? 64 : 32;
 }
-// Neighbouring tokens that a wave loads with one address where they lie in one
-// block: all of its quarter of a unit, or, in 4 bits, those of one load; 0: never.
+// Neighbouring tokens that are loaded with one address where they lie in one
+// block: all of a wave's quarter of a unit, or, in 4 bits, those of one load; 0: never.
 constexpr int attn_span(int D, int M, bool fp4) {
   return !fp4 ? attn_unit(D, M, fp4) / 4 : 64 % (D / 32) == 0 ? 64 / (D / 32) : 0;
 }
 
-inline Cut attn_cut(int R, int q_max, int n_q, int n_kv, int D, int type) {
+inline Cut attn_cut(int R, int q_max, int n_q, int n_kv, int D, int type, int bs) {
   Cut c;
-  c.M = attn_queries(q_max, n_q / n_kv, D);
-  c.TT = attn_unit(D, c.M, type == SD_CACHE_FP4);
-  c.W = 512;               // two workgroups with 64 KB of LDS on each of 256 CUs
+  const bool fp4 = type == SD_CACHE_FP4;
+  c.M = attn_queries(q_max, n_q / n_kv, D, fp4, bs);
+  c.direct = attn_direct(D, c.M, fp4, bs);
+  c.TT = c.direct ? 128 : attn_unit(D, c.M, fp4);
+  c.W = 512;               // two workgroups on each of 256 CUs, by their registers and LDS
   c.max_tiles = (long long)R * (((long long)q_max * (n_q / n_kv) + c.M - 1) / c.M);
   size_t at = 256;
   auto take = [&](size_t n) {
@@ -130,7 +143,7 @@ struct AttnArgs {
 
 SDV_DEV bool same_shape(const PlanShape& x, const PlanShape& y) {
   return x.mark == y.mark && x.R == y.R && x.q_max == y.q_max && x.n_q == y.n_q && x.n_kv == y.n_kv && x.D == y.D &&
-         x.type == y.type;
+         x.type == y.type && x.bs == y.bs;
 }
 
 // The plan knows neither the table's width nor the rows of the buffers.
@@ -141,5 +154,6 @@ SDV_DEV bool in_range(const AttnArgs& a, const Tile& t) {
 // One launch of the kernel for D, M and the cache's type.
 int attend_bf16(hipStream_t stream, int M, int W, const AttnArgs& a);
 int attend_fp4(hipStream_t stream, int M, int W, const AttnArgs& a);
+int attend_direct(hipStream_t stream, int M, int W, const AttnArgs& a);
 
 }  // namespace sdv

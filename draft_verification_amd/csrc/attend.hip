@@ -243,18 +243,19 @@ bool off256(const void* p) { return ((uintptr_t)p & 255) != 0; }
 
 extern "C" size_t sd_attn_workspace_size(int R, int q_max, int n_q, int n_kv, int D) {
   if (check_shape(R, q_max, n_q, n_kv, D, SD_CACHE_BF16) != SD_OK) return 0;
-  return attn_cut(R, q_max, n_q, n_kv, D, SD_CACHE_BF16).bytes;   // the same for both types
+  // tiles of 4 bits are as wide or narrower, and as many
+  return attn_cut(R, q_max, n_q, n_kv, D, SD_CACHE_BF16, 1).bytes;
 }
 
 extern "C" int sd_attn_plan(hipStream_t stream, int R, int q_max, int n_q, int n_kv, int D, int cache_type,
-                            const int32_t* row0, const int32_t* ell, const int32_t* ctx_len, int causal, int window,
+                            int block_size, const int32_t* row0, const int32_t* ell, const int32_t* ctx_len, int causal, int window,
                             int32_t* status, void* workspace, size_t workspace_bytes) {
   const int rc = check_shape(R, q_max, n_q, n_kv, D, cache_type);
   if (rc != SD_OK) return rc;
-  if ((causal != 0 && causal != 1) || window < 0) return SD_EINVAL;
+  if (block_size < 1 || (causal != 0 && causal != 1) || window < 0) return SD_EINVAL;
   if (R == 0) return SD_OK;
   if (!row0 || !ell || !ctx_len || !status || !workspace || off256(workspace)) return SD_EINVAL;
-  const Cut c = attn_cut(R, q_max, n_q, n_kv, D, cache_type);
+  const Cut c = attn_cut(R, q_max, n_q, n_kv, D, cache_type, block_size);
   if (workspace_bytes < c.bytes) return SD_ERANGE;
   const Span written[] = {span(status, 4ll * R), span(workspace, (long long)c.bytes)};
   const Span read[] = {span(row0, 4ll * R), span(ell, 4ll * R), span(ctx_len, 4ll * R)};
@@ -264,7 +265,7 @@ extern "C" int sd_attn_plan(hipStream_t stream, int R, int q_max, int n_q, int n
   a.row0 = row0, a.ell = ell, a.ctx = ctx_len, a.status = status;
   a.head = (PlanHead*)ws, a.tiles = (Tile*)(ws + c.tiles), a.sums = (long long*)(ws + c.sums);
   a.starts = (Start*)(ws + c.starts), a.cuts = (CutTile*)(ws + c.cuts);
-  a.shape = PlanShape{kPlanMark, R, q_max, n_q, n_kv, D, cache_type};
+  a.shape = PlanShape{kPlanMark, R, q_max, n_q, n_kv, D, cache_type, block_size};
   a.causal = causal, a.window = window, a.M = c.M, a.TT = c.TT, a.W = c.W, a.group = n_q / n_kv;
   SDV_TRY_LAUNCH(launch(k_plan, dim3(1), dim3(kPlanThreads), 0, stream, a));
   return SD_OK;
@@ -289,7 +290,7 @@ extern "C" int sd_cache_attn(hipStream_t stream, int R, int q_max, int n_q, int 
   if (cache_type == SD_CACHE_FP4 && (!k_scale || !v_scale)) return SD_EINVAL;
   if (off16(q) || off16(out) || off16(k_cache) || off16(v_cache) || off256(workspace)) return SD_EINVAL;
   if (ld_q < width || ld_q % 8 != 0 || ld_out < width || ld_out % 8 != 0) return SD_EINVAL;
-  const Cut c = attn_cut(R, q_max, n_q, n_kv, D, cache_type);
+  const Cut c = attn_cut(R, q_max, n_q, n_kv, D, cache_type, block_size);
   if (workspace_bytes < c.bytes) return SD_ERANGE;
   const bool fp4 = cache_type == SD_CACHE_FP4;
   const long long tokens = (long long)n_blocks * block_size * n_kv;
@@ -304,7 +305,7 @@ extern "C" int sd_cache_attn(hipStream_t stream, int R, int q_max, int n_q, int 
   AttnArgs a = {};
   a.q = q, a.out = out, a.lse = lse, a.ld_q = ld_q, a.ld_out = ld_out, a.table = block_table, a.status = status;
   a.cache = Cache{(void*)k_cache, (void*)v_cache, (uint8_t*)k_scale, (uint8_t*)v_scale, n_kv, block_size, n_blocks};
-  a.shape = PlanShape{kPlanMark, R, q_max, n_q, n_kv, D, cache_type};
+  a.shape = PlanShape{kPlanMark, R, q_max, n_q, n_kv, D, cache_type, block_size};
   a.max_blocks = max_blocks, a.n_rows = n_rows;
   a.head = (const PlanHead*)ws, a.tiles = (const Tile*)(ws + c.tiles), a.starts = (const Start*)(ws + c.starts);
   a.cuts = (const CutTile*)(ws + c.cuts);
@@ -319,7 +320,7 @@ extern "C" int sd_cache_attn(hipStream_t stream, int R, int q_max, int n_q, int 
   const int span = attn_span(D, c.M, fp4);
   a.once = (long long)q_max * (n_q / n_kv) <= c.M;
   a.spans = span > 0 && block_size % span == 0;
-  const int done = fp4 ? attend_fp4(stream, c.M, c.W, a) : attend_bf16(stream, c.M, c.W, a);
+  const int done = c.direct ? attend_direct(stream, c.M, c.W, a) : fp4 ? attend_fp4(stream, c.M, c.W, a) : attend_bf16(stream, c.M, c.W, a);
   if (done != SD_OK) return done;
 #define SDV_JOIN(DD) \
   case DD: SDV_TRY_LAUNCH(launch(k_join<DD>, dim3(kJoinGrid), dim3(kJoinThreads), 0, stream, a, c.M)); return SD_OK;

@@ -50,8 +50,16 @@ SDV_DEV void load_to_lds(const void* base, uint32_t off, uint32_t to) {   // bas
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base)
                  : "memory");
 }
+template <bool kOnce>
 SDV_DEV void load_to_lds(const void* from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+  if constexpr (kOnce)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(to), "v"(from) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+}
+// ... and 4 bytes per lane.
+SDV_DEV void load_word_to_lds(const void* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "memory");
 }
 SDV_DEV uint32_t lds_at(const void* p) { return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p; }
 
@@ -69,8 +77,9 @@ SDV_DEV float sum_over_groups(float v) {
 }
 
 // What every form of the kernel keeps of a tile: D channels, NT times 16
-// queries of a wave, 16 NS of its tokens at a time.
-template <int D, int NT, int NS, bool kFp4, bool kWide>
+// queries of a wave, 16 NS of its tokens at a time, of each 16 of which lane
+// group g has kByGroup g + kByPlace e, e < 4.
+template <int D, int NT, int NS, bool kFp4, bool kWide, int kByGroup = 4, int kByPlace = 1>
 struct Queries {
   static constexpr int KS = D / 32;           // steps of the sum over channels
   static constexpr int ND = D / 16;           // rows of O^T, 16 at a time
@@ -156,13 +165,13 @@ struct Queries {
   SDV_DEV void mask(int first, f32x4 (&s)[NS][NT]) const {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const uint32_t from = (uint32_t)(first + 4 * g) - (uint32_t)lo[nt];   // the lane's first token
+      const uint32_t from = (uint32_t)(first + kByGroup * g) - (uint32_t)lo[nt];   // the lane's first token
       const uint32_t span = (uint32_t)hi[nt] - (uint32_t)lo[nt];
 #pragma unroll
       for (int i = 0; i < NS; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (from + (i * 16 + e) >= span) s[i][nt][e] = -__builtin_huge_valf();
+          if (from + (i * 16 + kByPlace * e) >= span) s[i][nt][e] = -__builtin_huge_valf();
     }
   }
   // ... and of those outside the pool; returns which of the tokens are in it.
@@ -175,7 +184,7 @@ struct Queries {
       for (int e = 0; e < 4; ++e)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          if (i0 + i < NS && !(ok >> (i * 16 + 4 * g + e) & 1)) s[i0 + i < NS ? i0 + i : 0][nt][e] = -__builtin_huge_valf();
+          if (i0 + i < NS && !(ok >> (i * 16 + kByGroup * g + kByPlace * e) & 1)) s[i0 + i < NS ? i0 + i : 0][nt][e] = -__builtin_huge_valf();
     return ok;
   }
 
@@ -375,7 +384,7 @@ struct Kernel : Queries<D, NT, attn_unit(D, 64 / WT * NT, kFp4) / WT / 16, kFp4,
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
         const int c = (j * 64 + lane) % CH, swz = kValues ? swz_v(row_of(j)) : swz_k(row_of(j));
-        load_to_lds(head + place(token_of(u, j), b.of[j], bad) * kRow + (c ^ swz) * 16, to + j * 1024);
+        load_to_lds<false>(head + place(token_of(u, j), b.of[j], bad) * kRow + (c ^ swz) * 16, to + j * 1024);
       }
     }
     if (!kValues) note_bad(bad, buf);
@@ -801,19 +810,23 @@ __global__ __launch_bounds__(kAttnThreads, 2) void k_attend(AttnArgs a) {
 template <bool kFp4>
 int launch_attend(hipStream_t stream, int M, int W, const AttnArgs& a) {
   const dim3 grid((unsigned)W), block(kAttnThreads);
-#define SDV_ATTN(...) SDV_TRY_LAUNCH(sdv::launch(k_attend<__VA_ARGS__, kFp4>, grid, block, 0, stream, a))
-#define SDV_ATTN_SMALL(D)                                  \
-  case D:                                                  \
-    if (M == 16) SDV_ATTN(D, 1, 4);                        \
-    else if (M == 32) SDV_ATTN(D, 1, 2);                   \
-    else if (M == 64) SDV_ATTN(D, 2, 2);                   \
-    else SDV_ATTN(D, 2, 1);                                \
-    return SD_OK;
-#define SDV_ATTN_LARGE(D)                                  \
-  case D:                                                  \
-    if (M == 32) SDV_ATTN(D, 1, 2);                        \
-    else SDV_ATTN(D, 1, 1);                                \
-    return SD_OK;
+#define SDV_ATTN(...)                                                                            \
+  do {                                                                                           \
+    SDV_TRY_LAUNCH(sdv::launch(k_attend<__VA_ARGS__, kFp4>, grid, block, 0, stream, a));         \
+    return SD_OK;                                                                                \
+  } while (0)
+#define SDV_ATTN_SMALL(D)                                                                        \
+  case D:                                                                                        \
+    if (M == 16) SDV_ATTN(D, 1, 4);                                                              \
+    if (M == 32) SDV_ATTN(D, 1, 2);                                                              \
+    if (M == 64) SDV_ATTN(D, 2, 2);                                                              \
+    if (M == 128) SDV_ATTN(D, 2, 1);                                                             \
+    break;
+#define SDV_ATTN_LARGE(D)                                                                        \
+  case D:                                                                                        \
+    if (M == 32) SDV_ATTN(D, 1, 2);                                                              \
+    if (M == 64) SDV_ATTN(D, 1, 1);                                                              \
+    break;
   switch (a.shape.D) {
     SDV_ATTN_SMALL(64)
     SDV_ATTN_SMALL(96)

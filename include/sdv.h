@@ -692,7 +692,7 @@ int sd_cache_read(hipStream_t stream, int n_rows, int D, const int64_t* row_slot
  * (one per layer) are given.  Another mask needs a plan of its own.
  *   R >= 0; q_max >= 1 (rows of a request, as in sd_slot_reserve); n_q a
  *   multiple of n_kv; D 64, 96, 128, 192 or 256; R * q_max * n_q / n_kv below
- *   2^31 - 257; cache_type SD_CACHE_BF16 or SD_CACHE_FP4
+ *   2^31 - 257; cache_type SD_CACHE_BF16 or SD_CACHE_FP4; block_size >= 1
  *   status     [R] int32 out: BAD_INPUT where ctx_len is below the request's
  *              rows or past 2^31 - 257, or row0 is negative: its rows are
  *              left as they are
@@ -700,7 +700,7 @@ int sd_cache_read(hipStream_t stream, int n_rows, int D, const int64_t* row_slot
  *              aligned
  *
  * sd_cache_attn - one layer's attention with a plan.  R, q_max, n_q, n_kv, D,
- * cache_type as the plan's (with others nothing is written).
+ * cache_type, block_size as the plan's (with others nothing is written).
  *   q, out       [n_rows] rows of n_q heads, bf16, ld elements apart (ld % 8
  *                == 0), 16-byte aligned; rows of no request are left as they
  *                are in out
@@ -723,7 +723,7 @@ int sd_cache_read(hipStream_t stream, int n_rows, int D, const int64_t* row_slot
  */
 size_t sd_attn_workspace_size(int R, int q_max, int n_q, int n_kv, int D);
 int sd_attn_plan(hipStream_t stream, int R, int q_max, int n_q, int n_kv, int D, int cache_type,
-                 const int32_t* row0, const int32_t* ell, const int32_t* ctx_len, int causal, int window,
+                 int block_size, const int32_t* row0, const int32_t* ell, const int32_t* ctx_len, int causal, int window,
                  int32_t* status, void* workspace, size_t workspace_bytes);
 int sd_cache_attn(hipStream_t stream, int R, int q_max, int n_q, int n_kv, int D, int n_rows,
                   const uint16_t* q, long long ld_q, int cache_type, int block_size, int n_blocks,
