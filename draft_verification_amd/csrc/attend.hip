@@ -304,7 +304,7 @@ extern "C" int sd_cache_attn(hipStream_t stream, int R, int q_max, int n_q, int 
   char* ws = (char*)workspace;
   AttnArgs a = {};
   a.q = q, a.out = out, a.lse = lse, a.ld_q = ld_q, a.ld_out = ld_out, a.table = block_table, a.status = status;
-  a.cache = Cache{(void*)k_cache, (void*)v_cache, (uint8_t*)k_scale, (uint8_t*)v_scale, n_kv, block_size, n_blocks};
+  a.cache = Cache{(void*)k_cache, (void*)v_cache, (uint8_t*)k_scale, (uint8_t*)v_scale, n_kv, block_size, n_blocks, 1.0 / block_size};
   a.shape = PlanShape{kPlanMark, R, q_max, n_q, n_kv, D, cache_type, block_size};
   a.max_blocks = max_blocks, a.n_rows = n_rows;
   a.head = (const PlanHead*)ws, a.tiles = (const Tile*)(ws + c.tiles), a.starts = (const Start*)(ws + c.starts);

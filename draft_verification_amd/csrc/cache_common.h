@@ -14,11 +14,26 @@ struct Cache {
   uint8_t* k_scale;
   uint8_t* v_scale;
   int n_kv, bs, n_blocks;
+  double per_bs;   // 1 / bs
 };
 
 // Token (block, off) of head h, as an index of tokens.
 SDV_DEV int64_t cache_token(const Cache& c, int64_t block, int h, int off) {
   return (block * c.n_kv + h) * c.bs + off;
+}
+
+// Slot s as a block and an offset in it; false where it is outside the cache.
+// The block's number is below 2^31, so the quotient in fp64 is off by less than
+// one; it saves a division of 64-bit integers, some hundred instructions.
+SDV_DEV bool cache_slot(const Cache& c, int64_t s, int64_t* block, int* off) {
+  if (s < 0 || s >= (int64_t)c.n_blocks * c.bs) return false;
+  int64_t b = (int64_t)((double)s * c.per_bs);
+  int64_t o = s - b * c.bs;
+  if (o < 0) --b, o += c.bs;
+  if (o >= c.bs) ++b, o -= c.bs;
+  *block = b;
+  *off = (int)o;
+  return true;
 }
 
 // The scale byte (exponent + 127) of 32 channels whose largest magnitude has

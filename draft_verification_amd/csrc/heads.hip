@@ -43,18 +43,23 @@ struct HeadArgs {
 };
 
 // Eight channels as a lane holds them: four from `lo` on and four from `hi`.
-template <typename T>
-SDV_DEV void load_runs(const T* p, int lo, int hi, float (&x)[8]);
-template <>
-SDV_DEV void load_runs<uint16_t>(const uint16_t* p, int lo, int hi, float (&x)[8]) {
-  const uint2 a = *(const uint2*)(p + lo), b = *(const uint2*)(p + hi);
-  x[0] = sdv::bf16lo(a.x), x[1] = sdv::bf16hi(a.x), x[2] = sdv::bf16lo(a.y), x[3] = sdv::bf16hi(a.y);
-  x[4] = sdv::bf16lo(b.x), x[5] = sdv::bf16hi(b.x), x[6] = sdv::bf16lo(b.y), x[7] = sdv::bf16hi(b.y);
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+template <bool kStream, typename V>
+SDV_DEV V load_vec(const V* p) {
+  return kStream ? __builtin_nontemporal_load(p) : *p;
 }
-template <>
-SDV_DEV void load_runs<float>(const float* p, int lo, int hi, float (&x)[8]) {
-  const float4 a = *(const float4*)(p + lo), b = *(const float4*)(p + hi);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+template <bool kStream>
+SDV_DEV void load_runs(const uint16_t* p, int lo, int hi, float (&x)[8]) {
+  const u32x2 a = load_vec<kStream>((const u32x2*)(p + lo)), b = load_vec<kStream>((const u32x2*)(p + hi));
+  x[0] = sdv::bf16lo(a[0]), x[1] = sdv::bf16hi(a[0]), x[2] = sdv::bf16lo(a[1]), x[3] = sdv::bf16hi(a[1]);
+  x[4] = sdv::bf16lo(b[0]), x[5] = sdv::bf16hi(b[0]), x[6] = sdv::bf16lo(b[1]), x[7] = sdv::bf16hi(b[1]);
+}
+template <bool kStream>
+SDV_DEV void load_runs(const float* p, int lo, int hi, float (&x)[8]) {
+  const f32x4 a = load_vec<kStream>((const f32x4*)(p + lo)), b = load_vec<kStream>((const f32x4*)(p + hi));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = a[i], x[4 + i] = b[i];
 }
 SDV_DEV void store_runs(uint16_t* p, int lo, int hi, const float (&x)[8]) {
   *(uint2*)(p + lo) = make_uint2(sdv::pack_bf16(x[0], x[1]), sdv::pack_bf16(x[2], x[3]));
@@ -72,16 +77,24 @@ enum { kToRows = 0, kToBf16 = 1, kToFp4 = 2 };
 // D / 8 lanes of a group with eight channels each.  Lane c of a rotated head
 // has four pairs: with the halves paired, channels 4c.. and rot/2 + 4c..; with
 // neighbours paired, 8c.. ; so its four angles serve all heads of the row.
+// Into rows nothing but rows is read, and streaming loads win (16384 rows of 40
+// heads of 128: 53 us, 61 us with cached ones); into the cache they make no
+// difference (8192 rows of 80 heads into bf16: 68 us both ways).
 template <typename T, int kTo, bool kNeighbours>
 __global__ __launch_bounds__(kThreads) void k_heads(HeadArgs a) {
   // Channels in their order, for groups of 32: only 4 bits need them.
   __shared__ float order[kTo == kToFp4 ? kThreads * 8 : 1];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t job = (int64_t)blockIdx.x * kWaves + wave;
-  const int row = (int)(job / a.parts), part = (int)(job - (int64_t)row * a.parts);
+  const unsigned job = blockIdx.x * kWaves + wave;
+  const int row = (int)(job / (unsigned)a.parts), part = (int)(job - (unsigned)row * (unsigned)a.parts);
   if (row >= a.n_rows) return;
   const int pos = a.pos ? a.pos[row] : 0;
   if (pos < 0) return;
+  constexpr bool kStream = kTo == kToRows;
+  // Into 4 bits, where the arithmetic counts, values go a way of their own:
+  // their lanes hold neighbours, and a step of nothing but values has no norm
+  // and no exchange.  (Into bf16 the branches cost more: 76 us, 69 without.)
+  constexpr bool kApart = kTo == kToFp4;
   const int c = lane & (a.lanes - 1), group = lane / a.lanes, groups = 64 / a.lanes;
   const int heads = a.n_q + a.n_kv + a.n_v;
   const bool in = c * 8 < a.D, turned = c * 8 < a.rot;
@@ -91,11 +104,7 @@ __global__ __launch_bounds__(kThreads) void k_heads(HeadArgs a) {
   int64_t block = -1;
   int off = 0;
   if constexpr (kTo != kToRows) {
-    const int64_t s = a.slot[row];
-    if (s >= 0 && s < (int64_t)a.cache.n_blocks * a.cache.bs) {
-      block = s / a.cache.bs;
-      off = (int)(s - block * a.cache.bs);
-    }
+    if (!sdv::cache_slot(a.cache, a.slot[row], &block, &off)) block = -1;
   }
   const int first = part * a.iters * groups + group;
   auto at = [&](int h) -> const T* {
@@ -103,8 +112,13 @@ __global__ __launch_bounds__(kThreads) void k_heads(HeadArgs a) {
     if (h < a.n_q + a.n_kv) return (const T*)a.k + row * a.ld_k + (int64_t)(h - a.n_q) * a.D;
     return (const T*)a.v + row * a.ld_v + (int64_t)(h - a.n_q - a.n_kv) * a.D;
   };
+  const int first_v = a.n_q + a.n_kv;
+  auto load = [&](int h, float (&to)[8]) {
+    const bool apart = kApart && h >= first_v;
+    if (in && h < heads) load_runs<kStream>(at(h), apart ? 8 * c : lo, apart ? 8 * c + 4 : hi, to);
+  };
   float x[8] = {}, next[8] = {};
-  if (in && first < heads) load_runs<T>(at(first), lo, hi, next);   // while the angles are formed
+  load(first, next);   // while the angles are formed
 
   float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {};
   if (turned) {
@@ -119,17 +133,18 @@ __global__ __launch_bounds__(kThreads) void k_heads(HeadArgs a) {
   float wq[8], wk[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) wq[i] = wk[i] = 1.f;
-  if (in && a.wq) load_runs<float>(a.wq, lo, hi, wq);
-  if (in && a.wk) load_runs<float>(a.wk, lo, hi, wk);
+  if (in && a.wq) load_runs<false>(a.wq, lo, hi, wq);
+  if (in && a.wk) load_runs<false>(a.wk, lo, hi, wk);
 
   for (int it = 0; it < a.iters; ++it) {
     const int h = first + it * groups;
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = next[i];
     const bool live = h < heads;
-    if (in && it + 1 < a.iters && h + groups < heads) load_runs<T>(at(h + groups), lo, hi, next);
-    const bool is_q = h < a.n_q, is_v = h >= a.n_q + a.n_kv;
-    if (a.wq || a.wk) {   // uniform over the grid
+    if (it + 1 < a.iters) load(h + groups, next);
+    const bool is_q = h < a.n_q, is_v = h >= first_v;
+    const bool some = !kApart || __ballot(!is_v) != 0;   // heads of the step that are no values
+    if (some && (a.wq || a.wk)) {
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) s += x[i] * x[i];
@@ -158,25 +173,27 @@ __global__ __launch_bounds__(kThreads) void k_heads(HeadArgs a) {
       if (live && in) store_runs((T*)a.k_out + row * a.ld_ko + (int64_t)hk * a.D, lo, hi, x);
     } else if constexpr (kTo == kToBf16) {
       if (live && in && block >= 0)
-        store_runs((uint16_t*)(is_v ? a.cache.v : a.cache.k) + sdv::cache_token(a.cache, block, hk, off) * a.D, lo,
-                   hi, x);
+        store_runs((uint16_t*)(is_v ? a.cache.v : a.cache.k) + sdv::cache_token(a.cache, block, hk, off) * a.D,
+                   lo, hi, x);
     } else {
-      // Through LDS into the channels' order: lane c then has 8c .. 8c + 7,
+      // Keys through LDS into the channels' order: lane c then has 8c .. 8c + 7,
       // and four neighbours a group of 32.  A wave's own part: its LDS
       // accesses are done in order, so no barrier is needed.
-      float* o = order + wave * 512 + group * a.lanes * 8;
-      *(float4*)(o + lo) = make_float4(x[0], x[1], x[2], x[3]);
-      *(float4*)(o + hi) = make_float4(x[4], x[5], x[6], x[7]);
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      const float4 y = *(const float4*)(o + 8 * c), z = *(const float4*)(o + 8 * c + 4);
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();   // the next step's stores stay behind these loads
-      float n[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+      if (some && !kNeighbours && a.rot > 0) {
+        float* o = order + wave * 512 + group * a.lanes * 8;
+        *(float4*)(o + (is_v ? 8 * c : lo)) = make_float4(x[0], x[1], x[2], x[3]);
+        *(float4*)(o + (is_v ? 8 * c + 4 : hi)) = make_float4(x[4], x[5], x[6], x[7]);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const float4 y = *(const float4*)(o + 8 * c), z = *(const float4*)(o + 8 * c + 4);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();   // the next step's stores stay behind these loads
+        x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w, x[4] = z.x, x[5] = z.y, x[6] = z.z, x[7] = z.w;
+      }
       uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint32_t b = __float_as_uint(n[i]) & 0x7FFFFFFFu;   // ordered as the magnitudes, NaN last
+        const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;   // ordered as the magnitudes, NaN last
         top = top > b ? top : b;
       }
 #pragma unroll
@@ -185,7 +202,7 @@ __global__ __launch_bounds__(kThreads) void k_heads(HeadArgs a) {
         top = top > b ? top : b;
       }
       const uint32_t byte = sdv::fp4_scale_byte(top);
-      const uint32_t codes = byte == 255u ? 0u : sdv::fp4_from_f32(n, sdv::fp4_scale(byte));
+      const uint32_t codes = byte == 255u ? 0u : sdv::fp4_from_f32(x, sdv::fp4_scale(byte));
       if (live && in && !is_q && block >= 0) {
         const int64_t t = sdv::cache_token(a.cache, block, hk, off);
         ((uint32_t*)(is_v ? a.cache.v : a.cache.k))[t * (a.D / 8) + c] = codes;
@@ -205,40 +222,41 @@ struct ReadArgs {
   int vecs;   // of eight channels per row, both sides
 };
 
-// One thread per eight channels of a row's keys or values.
+// A workgroup per row, a thread per eight channels of its keys or values.
 template <typename T, bool kFp4>
 __global__ __launch_bounds__(kThreads) void k_cache_read(ReadArgs a) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int row = (int)(i / a.vecs);
-  if (row >= a.n_rows) return;
-  int e = (int)(i - (int64_t)row * a.vecs);
-  const int64_t s = a.slot[row];
-  if (s < 0 || s >= (int64_t)a.cache.n_blocks * a.cache.bs) return;
-  const int64_t block = s / a.cache.bs;
-  const bool is_v = e >= a.vecs / 2;
-  if (is_v) e -= a.vecs / 2;
-  const int h = e / (a.D / 8), c = e - h * (a.D / 8);
-  const int64_t t = sdv::cache_token(a.cache, block, h, (int)(s - block * a.cache.bs));
-  const void* side = is_v ? a.cache.v : a.cache.k;
-  uint4 w;
-  if constexpr (kFp4) {
-    const uint8_t byte = (is_v ? a.cache.v_scale : a.cache.k_scale)[t * (a.D / 32) + (c >> 2)];
-    w = sdv::fp4_to_bf16(((const uint32_t*)side)[t * (a.D / 8) + c], sdv::fp4_scale(byte));
-  } else {
-    w = ((const uint4*)side)[t * (a.D / 8) + c];
-  }
-  T* out = (is_v ? (T*)a.v_out + row * a.ld_v : (T*)a.k_out + row * a.ld_k) + (int64_t)h * a.D + 8 * c;
-  if constexpr (sizeof(T) == 2) {
-    *(uint4*)out = w;
-  } else {
-    *(float4*)out = make_float4(sdv::bf16lo(w.x), sdv::bf16hi(w.x), sdv::bf16lo(w.y), sdv::bf16hi(w.y));
-    *(float4*)(out + 4) = make_float4(sdv::bf16lo(w.z), sdv::bf16hi(w.z), sdv::bf16lo(w.w), sdv::bf16hi(w.w));
+  const int row = blockIdx.x;
+  int64_t block;
+  int off;
+  if (!sdv::cache_slot(a.cache, a.slot[row], &block, &off)) return;
+  for (int i = threadIdx.x; i < a.vecs; i += blockDim.x) {
+    const bool is_v = i >= a.vecs / 2;
+    const int e = is_v ? i - a.vecs / 2 : i;
+    const int h = (int)((unsigned)e / (unsigned)(a.D / 8)), c = e - h * (a.D / 8);
+    const int64_t t = sdv::cache_token(a.cache, block, h, off);
+    const void* side = is_v ? a.cache.v : a.cache.k;
+    uint4 w;
+    if constexpr (kFp4) {
+      const uint8_t byte = (is_v ? a.cache.v_scale : a.cache.k_scale)[t * (a.D / 32) + (c >> 2)];
+      w = sdv::fp4_to_bf16(((const uint32_t*)side)[t * (a.D / 8) + c], sdv::fp4_scale(byte));
+    } else {
+      w = ((const uint4*)side)[t * (a.D / 8) + c];
+    }
+    T* out = (is_v ? (T*)a.v_out + row * a.ld_v : (T*)a.k_out + row * a.ld_k) + (int64_t)h * a.D + 8 * c;
+    if constexpr (sizeof(T) == 2) {
+      *(uint4*)out = w;
+    } else {
+      *(float4*)out = make_float4(sdv::bf16lo(w.x), sdv::bf16hi(w.x), sdv::bf16lo(w.y), sdv::bf16hi(w.y));
+      *(float4*)(out + 4) = make_float4(sdv::bf16lo(w.z), sdv::bf16hi(w.z), sdv::bf16lo(w.w), sdv::bf16hi(w.w));
+    }
   }
 }
 
 // Waves that fill the chip several times over; past them a wave takes more of
-// its row's heads, whose angles it forms once.
-constexpr long long kEnoughWaves = 8192;
+// its row's heads, whose angles it forms once.  With 16384 and 8192 of them,
+// 8192 rows of 64 heads and 16 into a bf16 cache take 69 and 76 us, and 16
+// heads a row into 4 bits, with their reading back, 44 and 41 us.
+constexpr long long kEnoughWaves = 16384, kEnoughWavesFp4 = 8192;
 
 int run_heads(hipStream_t stream, HeadArgs& a, int dtype, int to, bool neighbours) {
   const int heads = a.n_q + a.n_kv + a.n_v;
@@ -246,7 +264,8 @@ int run_heads(hipStream_t stream, HeadArgs& a, int dtype, int to, bool neighbour
   while (a.lanes * 8 < a.D) a.lanes *= 2;
   if (to == kToFp4 && a.lanes < 4) a.lanes = 4;
   const int steps = (heads + 64 / a.lanes - 1) / (64 / a.lanes);
-  const long long iters = ((long long)a.n_rows * steps + kEnoughWaves - 1) / kEnoughWaves;
+  const long long waves = to == kToFp4 ? kEnoughWavesFp4 : kEnoughWaves;
+  const long long iters = ((long long)a.n_rows * steps + waves - 1) / waves;
   a.iters = (int)(iters < steps ? iters : steps);
   a.parts = (steps + a.iters - 1) / a.iters;
   const long long groups = ((long long)a.n_rows * a.parts + kWaves - 1) / kWaves;
@@ -374,7 +393,7 @@ extern "C" int sd_cache_append(hipStream_t stream, int n_rows, int D, int dtype,
   a.ld_q = ld_q, a.ld_k = ld_k, a.ld_v = ld_v, a.ld_qo = ld_q_out;
   a.pos = row_pos, a.slot = row_slot, a.wq = q_weight, a.wk = k_weight, a.inv_freq = inv_freq, a.eps = eps;
   a.n_rows = n_rows, a.n_q = n_q, a.n_kv = n_kv, a.n_v = n_kv, a.D = D, a.rot = rot_dim;
-  a.cache = Cache{k_cache, v_cache, k_scale, v_scale, n_kv, block_size, n_blocks};
+  a.cache = Cache{k_cache, v_cache, k_scale, v_scale, n_kv, block_size, n_blocks, 1.0 / block_size};
   return run_heads(stream, a, dtype, cache_type == SD_CACHE_FP4 ? kToFp4 : kToBf16, interleaved != 0);
 }
 
@@ -396,11 +415,11 @@ extern "C" int sd_cache_read(hipStream_t stream, int n_rows, int D, const int64_
   if (sdv::overlap(written, read)) return SD_EINVAL;
   ReadArgs a = {};
   a.slot = row_slot, a.k_out = k_out, a.v_out = v_out, a.ld_k = ld_k, a.ld_v = ld_v;
-  a.cache = Cache{(void*)k_cache, (void*)v_cache, (uint8_t*)k_scale, (uint8_t*)v_scale, n_kv, block_size, n_blocks};
+  a.cache = Cache{(void*)k_cache, (void*)v_cache, (uint8_t*)k_scale, (uint8_t*)v_scale, n_kv, block_size, n_blocks, 1.0 / block_size};
   a.n_rows = n_rows, a.D = D, a.vecs = 2 * n_kv * (D / 8);
-  const long long groups = ((long long)n_rows * a.vecs + kThreads - 1) / kThreads;
-  if (groups * kThreads > 0xFFFFFFFFll) return SD_EUNSUPPORTED;
-  const dim3 grid((unsigned)groups), block(kThreads);
+  const int threads = a.vecs < kThreads ? (a.vecs + 63) / 64 * 64 : kThreads;
+  if ((long long)n_rows * threads > 0xFFFFFFFFll) return SD_EUNSUPPORTED;
+  const dim3 grid((unsigned)n_rows), block((unsigned)threads);
   if (cache_type == SD_CACHE_FP4) {
     if (es == 4) SDV_TRY_LAUNCH(sdv::launch(k_cache_read<float, true>, grid, block, 0, stream, a));
     else SDV_TRY_LAUNCH(sdv::launch(k_cache_read<uint16_t, true>, grid, block, 0, stream, a));
