@@ -34,6 +34,7 @@ struct PlanHead {
   int n_tiles;
   int n_cuts;
   int slices;                // of a cut tile's parts, joined side by side
+  int lead;                  // units that the beginning of a tile counts as
   long long total, quota;    // units: of all heads, per workgroup
 };
 
@@ -44,8 +45,8 @@ struct Tile {
   int ctx, row0, n;  // tokens, first row and rows of the request
 };
 
-// Where a workgroup's run begins: off units into tile `index`, a copy of which
-// is here, so that a run begins with one read.
+// Where a workgroup's run begins: off units into tile `index` (its lead first),
+// a copy of which is here, so that a run begins with one read.
 struct Start {
   Tile tile;
   int head, index, off, pad;

@@ -97,6 +97,7 @@ struct Queries {
   const int32_t* table;           // the request's row
   bool causal;
   int window;
+  int turn;                       // which of a CU's two workgroups this is likely to be
   b16x8 qf[NT][KS];
   f32x4 o[ND][NT];
   float m[NT], l[NT];
@@ -775,21 +776,25 @@ SDV_DEV void run_tiles(const AttnArgs& a, typename K::Shared& sh) {
   K k(a, sh);
   k.causal = p.causal != 0;
   k.window = p.window;
+  k.turn = (int)(blockIdx.x / (gridDim.x / 2));
   Start s = uniform(a.starts[w]);
-  const int n_tiles = p.n_tiles;
+  const int n_tiles = p.n_tiles, lead = p.lead;
   for (;;) {
     const Tile& t = s.tile;
     const long long room = end - at;
-    const int left = t.units - s.off, n = left < room ? left : (int)room;
-    if (in_range(a, t)) {
+    const int left = lead + t.units - s.off, take = left < room ? left : (int)room;
+    const int first = max(s.off - lead, 0), n = s.off + take - lead - first;
+    if (n <= 0) {
+      // no more than the tile's lead
+    } else if (in_range(a, t)) {
       k.begin(t, s.head);
-      k.units(t.u0 + s.off, n);
+      k.units(t.u0 + first, n);
       // a part that begins its tile goes to the run's second place, others to its first
-      k.end(n == t.units ? -1 : s.off == 0 ? 2 * w + 1 : 2 * w);
+      k.end(n == t.units ? -1 : first == 0 ? 2 * w + 1 : 2 * w);
     } else if (threadIdx.x == 0) {
       atomicOr(a.status + t.req, SD_ST_BAD_INPUT);
     }
-    at += n;
+    at += take;
     if (at >= end) break;
     s.off = 0;
     if (++s.index == n_tiles) {

@@ -321,6 +321,31 @@ def test_forms(kind, bs, D, n_q, n_kv, q_max):
                   visible(n, T, True, mask.get("window", 0)), float(np.float32(D ** -0.5)), (r, mask))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp4"])
+@pytest.mark.parametrize("q_max", [3, 40])
+def test_many_units_to_a_run(kind, q_max):
+    """Enough work for long runs of the 512 workgroups, in tiles of one unit and
+    of a hundred: requests share the pool's blocks, each in an order of its own."""
+    g = gen(51)
+    R, n_q, n_kv, D, bs, blocks = 160, 16, 8, 64, 16, 420
+    n = torch.randint(1, q_max + 1, (R,), generator=g)
+    ctx = torch.maximum(torch.exp(torch.rand(R, generator=g) * 8.8).long(), n)
+    n[0], ctx[0], n[5], ctx[7] = q_max, bs * blocks, 0, 6000
+    row0 = torch.cumsum(n, 0) - n
+    table = torch.stack([torch.randperm(blocks, generator=g) for _ in range(R)]).to(torch.int32)
+    cache, sides = random_cache(g, kind, blocks, n_kv, bs, D)
+    q = torch.randn((int(n.sum()), n_q, D), generator=g).to(torch.bfloat16).to(DEV)
+    assert int(((ctx + 127) // 128)[n > 0].sum()) * n_kv > 16 * 512
+    b = dict(q=q, cache=cache, dev_table=table.to(DEV), args=(_t(row0), _t(n - 1), _t(ctx)), q_max=q_max, n_q=n_q)
+    got = [np64(t) for t in _attend(b)]
+    assert not got[2].any()
+    for r in range(R):
+        m, T, r0 = int(n[r]), int(ctx[r]), int(row0[r])
+        if m:
+            k, v = (tokens_of(x, table, r, T, bs) for x in sides)
+            check(got[0][r0:r0 + m], got[1][r0:r0 + m], np64(q)[r0:r0 + m], k, v, visible(m, T, True, 0), 0.125, r)
+
+
 def test_single_rows_no_rows_and_refusals():
     """A single row's stride says nothing, and an empty step is no error."""
     b = _batch(41, "bf16", 1, 1, 4, 2, 64, 16, 50, 50)
