@@ -740,10 +740,11 @@ def _heads(t, dtype, name, index, shape=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != index:
         raise ValueError(f"{name} must live on cuda:{index}, not {t.device}")
-    if t.dim() != 3 or (shape is not None and t.shape != shape):
+    got = t.shape
+    if len(got) != 3 or (shape is not None and got != shape):
         raise ValueError(f"{name} must be [rows][heads][D]{'' if shape is None else f' {list(shape)}'}, "
-                         f"got shape {list(t.shape)}")
-    n, h, d = t.shape
+                         f"got shape {list(got)}")
+    n, h, d = got
     s0, s1, s2 = t.stride()
     if (s2 != 1 and d > 1) or (s1 != d and h > 1):
         raise ValueError(f"{name}: the heads of a row must lie together, got strides {[s0, s1, s2]}")
@@ -767,9 +768,10 @@ def _rotation(inv_freq, pos, D, what):
         return 0
     if pos is None:
         raise ValueError(f"inv_freq needs {what}")
-    if 2 * inv_freq.numel() > D:
-        raise ValueError(f"inv_freq holds {inv_freq.numel()} pairs, a head {D} channels")
-    return 2 * inv_freq.numel()
+    pairs = inv_freq.numel()
+    if 2 * pairs > D:
+        raise ValueError(f"inv_freq holds {pairs} pairs, a head {D} channels")
+    return 2 * pairs
 
 
 def _cache_args(cache, index):
@@ -777,19 +779,24 @@ def _cache_args(cache, index):
     bf16, or (k, v, k_scale, v_scale) uint8 in 4 bits."""
     if not isinstance(cache, (tuple, list)) or len(cache) not in (2, 4):
         raise ValueError("cache must be (k, v) or (k, v, k_scale, v_scale)")
-    k, v = cache[0], cache[1]
-    dt = torch.bfloat16 if len(cache) == 2 else torch.uint8
-    at = [_arg(k, dt, "k cache", index), _arg(v, dt, "v cache", index), None, None]
-    if k is None or v is None or k.dim() != 4 or k.shape != v.shape:
+    if len(cache) == 2:
+        (k, v), dt, ctype = cache, torch.bfloat16, SD_CACHE_BF16
+    else:
+        (k, v, k_scale, v_scale), dt, ctype = cache, torch.uint8, SD_CACHE_FP4
+    at_k, at_v = _arg(k, dt, "k cache", index), _arg(v, dt, "v cache", index)
+    shape = None if k is None or v is None else k.shape
+    if shape is None or len(shape) != 4 or v.shape != shape:
         raise ValueError("the caches must be [n_blocks][n_kv][block_size][channels] and alike")
-    n_blocks, n_kv, bs, D = k.shape
-    if len(cache) == 4:
-        D *= 2
-        for i, name in ((2, "k_scale"), (3, "v_scale")):
-            at[i] = _arg(cache[i], dt, name, index)
-            if cache[i] is None or cache[i].shape != (n_blocks, n_kv, bs, D // 32):
-                raise ValueError(f"{name} must be [n_blocks][n_kv][block_size][D / 32]")
-    return (SD_CACHE_BF16 if len(cache) == 2 else SD_CACHE_FP4), n_blocks, n_kv, bs, D, at
+    n_blocks, n_kv, bs, D = shape
+    if ctype == SD_CACHE_BF16:
+        return ctype, n_blocks, n_kv, bs, D, (at_k, at_v, None, None)
+    D *= 2
+    at_ks, at_vs = _arg(k_scale, dt, "k_scale", index), _arg(v_scale, dt, "v_scale", index)
+    groups = (n_blocks, n_kv, bs, D // 32)
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t is None or t.shape != groups:
+            raise ValueError(f"{name} must be [n_blocks][n_kv][block_size][D / 32]")
+    return ctype, n_blocks, n_kv, bs, D, (at_k, at_v, at_ks, at_vs)
 
 
 @_on_device
