@@ -771,19 +771,28 @@ SDV_DEV void run_tiles(const AttnArgs& a, typename K::Shared& sh) {
   if (!same_shape(p.shape, a.shape)) return;
   const long long quota = p.quota, total = p.total;
   long long at = w * quota;
-  const long long end = at + quota < total ? at + quota : total;
+  long long end = at + quota < total ? at + quota : total;
   if (at >= end) return;
   K k(a, sh);
   k.causal = p.causal != 0;
   k.window = p.window;
   k.turn = (int)(blockIdx.x / (gridDim.x / 2));
-  Start s = uniform(a.starts[w]);
   const int n_tiles = p.n_tiles, lead = p.lead;
+  // Where requests have several tiles, the one that begins in this run and ends
+  // in another comes first: runs of a request are then at the same tokens at
+  // about the same time, and more of them are found in the cache that they
+  // share (16 requests with pieces of up to 512 rows, 8 key heads of 128: 226
+  // us, 237 in the tiles' order).
+  Start s = {};
+  if (!a.once && w + 1 < (int)gridDim.x) s = uniform(a.starts[w + 1]);
+  bool begins = s.off > lead && s.off - quota <= lead;
+  if (begins) end -= s.off;
+  else s = uniform(a.starts[w]);
   for (;;) {
     const Tile& t = s.tile;
     const long long room = end - at;
     const int left = lead + t.units - s.off, take = left < room ? left : (int)room;
-    const int first = max(s.off - lead, 0), n = s.off + take - lead - first;
+    const int first = begins ? 0 : max(s.off - lead, 0), n = s.off + (begins ? 0 : take) - lead - first;
     if (n <= 0) {
       // no more than the tile's lead
     } else if (in_range(a, t)) {
@@ -793,6 +802,12 @@ SDV_DEV void run_tiles(const AttnArgs& a, typename K::Shared& sh) {
       k.end(n == t.units ? -1 : first == 0 ? 2 * w + 1 : 2 * w);
     } else if (threadIdx.x == 0) {
       atomicOr(a.status + t.req, SD_ST_BAD_INPUT);
+    }
+    if (begins) {
+      if (at >= end) break;
+      begins = false;
+      s = uniform(a.starts[w]);
+      continue;
     }
     at += take;
     if (at >= end) break;
