@@ -55,7 +55,8 @@ SDV_DEV long long block_scan(long long v, long long* part, long long* total) {
 }
 
 // One workgroup: the tiles of all requests, the units before each of them, and
-// where every run begins.
+// where every run begins.  A chain of small reads, once per step: 12 us for 4
+// requests, 17 us for 128 (some 60 layers' calls share it).
 __global__ __launch_bounds__(kPlanThreads) void k_plan(PlanArgs a) {
   __shared__ long long part[kPlanThreads / 64];
   const int R = a.shape.R;
@@ -159,6 +160,10 @@ constexpr int kJoinQueries = 4;   // of a thread, whose loads are on their way t
 
 // Joins the parts of cut tiles, in the order of the runs: D / 4 threads to a
 // query and a slice of its parts (every slices-th one), slices through LDS.
+// With part p's maximum m_p, sum l_p and values o_p, and m the largest m_p:
+// out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p.  Two parts a run are
+// read at most: 5.5 us for tiles of 16 queries by 128 channels, 16 us for tiles
+// of 128 (64 MB at most, most of it still in the caches); latency bounds both.
 template <int D>
 __global__ __launch_bounds__(kJoinThreads) void k_join(AttnArgs a, int M) {
   constexpr int TQ = D / 4, QB = kJoinThreads / TQ, NQ = kJoinQueries;

@@ -820,6 +820,12 @@ SDV_DEV void run_tiles(const AttnArgs& a, typename K::Shared& sh) {
   }
 }
 
+// 128 contexts of 1024 to 16384 tokens, one row each, 32 heads on 8 of 128, bf16:
+// 455 to 464 us for 2.9 GB, 6.3 TB/s, bound by the memory.  Verify rows (up to
+// 12) over 512 to 8192 tokens: 274 us for 1.45 GB, 5.3 TB/s: the beginnings of
+// tiles and the two products.  Pieces of prompts, 0.18 Tflop: 210 us, 0.84
+// Pflop/s: of a SIMD's cycles the matrix cores work for 36 %, the vector units
+// for 43 %, mostly one after the other.
 template <int D, int NT, int WT, bool kFp4>
 __global__ __launch_bounds__(kAttnThreads, 2) void k_attend(AttnArgs a) {
   using K = Kernel<D, NT, WT, kFp4>;
