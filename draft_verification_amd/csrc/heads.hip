@@ -35,7 +35,7 @@ struct HeadArgs {
   const float* wk;
   const float* inv_freq;
   Cache cache;
-  float eps;
+  float eps, per_D;   // 1 / D
   int n_rows, n_q, n_kv, n_v, D, rot;
   int lanes;   // per head, a power of two
   int iters;   // steps of 64 / lanes heads that a wave takes
@@ -70,6 +70,26 @@ SDV_DEV void store_runs(float* p, int lo, int hi, const float (&x)[8]) {
   *(float4*)(p + hi) = make_float4(x[4], x[5], x[6], x[7]);
 }
 
+// A lane gets the value of lane ^ 1, lane ^ 2; of 8, of 16 mirrored.
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;
+template <int kFrom>
+SDV_DEV float other(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), kFrom, 0xF, 0xF, true));
+}
+// Over the `lanes` lanes (1 to 32) of each group, within the vector unit: an
+// exchange through LDS takes longer than all else in a step.
+SDV_DEV float sum_over_lanes(float v, int lanes) {
+  if (lanes > 1) v += other<kXor1>(v);
+  if (lanes > 2) v += other<kXor2>(v);
+  if (lanes > 4) v += other<kMirror8>(v);
+  if (lanes > 8) v += other<kMirror16>(v);
+  if (lanes > 16) {
+    const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+  }
+  return v;
+}
+
 // Where keys and values go.
 enum { kToRows = 0, kToBf16 = 1, kToFp4 = 2 };
 
@@ -80,9 +100,10 @@ enum { kToRows = 0, kToBf16 = 1, kToFp4 = 2 };
 // Into rows nothing but rows is read, and streaming loads win (16384 rows of 40
 // heads of 128: 53 us, 61 us with cached ones); into the cache they make no
 // difference (8192 rows of 80 heads into bf16: 68 us both ways).
-// Bound by the memory where calls are large: those rows move at 4.8 TB/s, into
-// bf16 at 4.4.  Into 4 bits the vector units bound it (8192 rows of 16 heads:
-// 20 us for 37 MB).  One row of a step: 3.5 us, the chain above.
+// Bound by the memory and the vector units where calls are large: those rows move
+// at 4.8 TB/s, into
+// bf16 at 4.4.  Into 4 bits the vector units alone bound it (8192 rows of 16 heads:
+// 19 us for 37 MB).  One row of a step: 3.5 us, the chain above.
 template <typename T, int kTo, bool kNeighbours>
 __global__ __launch_bounds__(kThreads) void k_heads(HeadArgs a) {
   // Channels in their order, for groups of 32: only 4 bits need them.
@@ -151,8 +172,8 @@ __global__ __launch_bounds__(kThreads) void k_heads(HeadArgs a) {
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) s += x[i] * x[i];
-      for (int o = a.lanes >> 1; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
-      const float r = 1.0f / sqrtf(s / (float)a.D + a.eps);
+      s = sum_over_lanes(s, a.lanes);
+      const float r = rsqrtf(s * a.per_D + a.eps);
       if (!is_v && (is_q ? a.wq : a.wk)) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (is_q ? wq[i] : wk[i]);
@@ -199,11 +220,8 @@ __global__ __launch_bounds__(kThreads) void k_heads(HeadArgs a) {
         const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;   // ordered as the magnitudes, NaN last
         top = top > b ? top : b;
       }
-#pragma unroll
-      for (int d = 1; d < 4; d <<= 1) {
-        const uint32_t b = __shfl_xor(top, d, 64);
-        top = top > b ? top : b;
-      }
+      top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, kXor1, 0xF, 0xF, true));
+      top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, kXor2, 0xF, 0xF, true));
       const uint32_t byte = sdv::fp4_scale_byte(top);
       const uint32_t codes = byte == 255u ? 0u : sdv::fp4_from_f32(x, sdv::fp4_scale(byte));
       if (live && in && !is_q && block >= 0) {
@@ -266,6 +284,7 @@ constexpr long long kEnoughWaves = 16384, kEnoughWavesFp4 = 8192;
 
 int run_heads(hipStream_t stream, HeadArgs& a, int dtype, int to, bool neighbours) {
   const int heads = a.n_q + a.n_kv + a.n_v;
+  a.per_D = 1.0f / a.D;
   a.lanes = 1;
   while (a.lanes * 8 < a.D) a.lanes *= 2;
   if (to == kToFp4 && a.lanes < 4) a.lanes = 4;
