@@ -303,7 +303,7 @@ extern "C" int sd_cache_attn(hipStream_t stream, int R, int q_max, int n_q, int 
   if (R == 0 || n_rows == 0) return SD_OK;
   const long long width = (long long)n_q * D;
   if (!q || !out || !k_cache || !v_cache || !block_table || !status || !workspace || n_blocks < 1) return SD_EINVAL;
-  if (cache_type == SD_CACHE_FP4 && (!k_scale || !v_scale)) return SD_EINVAL;
+  if (cache_type == SD_CACHE_FP4 && (!k_scale || !v_scale || off16(k_scale) || off16(v_scale))) return SD_EINVAL;
   if (off16(q) || off16(out) || off16(k_cache) || off16(v_cache) || off256(workspace)) return SD_EINVAL;
   if (ld_q < width || ld_q % 8 != 0 || ld_out < width || ld_out % 8 != 0) return SD_EINVAL;
   const Cut c = attn_cut(R, q_max, n_q, n_kv, D, cache_type, block_size);

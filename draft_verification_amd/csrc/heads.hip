@@ -100,10 +100,10 @@ enum { kToRows = 0, kToBf16 = 1, kToFp4 = 2 };
 // Into rows nothing but rows is read, and streaming loads win (16384 rows of 40
 // heads of 128: 53 us, 61 us with cached ones); into the cache they make no
 // difference (8192 rows of 80 heads into bf16: 68 us both ways).
-// Bound by the memory and the vector units where calls are large: those rows move
-// at 4.8 TB/s, into
-// bf16 at 4.4.  Into 4 bits the vector units alone bound it (8192 rows of 16 heads:
-// 19 us for 37 MB).  One row of a step: 3.5 us, the chain above.
+// Bound by the memory and the vector units where calls are large: those rows
+// move at 4.8 TB/s, into bf16 at 4.4.  Into 4 bits the vector units alone bound
+// it (8192 rows of 16 heads: 19 us for 37 MB).  A few rows: 3.5 us, the chain
+// above.
 template <typename T, int kTo, bool kNeighbours>
 __global__ __launch_bounds__(kThreads) void k_heads(HeadArgs a) {
   // Channels in their order, for groups of 32: only 4 bits need them.
@@ -342,7 +342,7 @@ int check_cache(int type, int n_kv, int D, int bs, int n_blocks, const void* k, 
   if (n_kv < 1 || bs < 1 || n_blocks < 0) return SD_EINVAL;
   if (type == SD_CACHE_FP4 && D % 32 != 0) return SD_EINVAL;
   if (!k || !v || off16(k) || off16(v)) return SD_EINVAL;
-  if (type == SD_CACHE_FP4 && (!ks || !vs)) return SD_EINVAL;
+  if (type == SD_CACHE_FP4 && (!ks || !vs || off16(ks) || off16(vs))) return SD_EINVAL;
   if ((long long)n_blocks * bs > (1ll << 40)) return SD_EUNSUPPORTED;
   const long long tokens = (long long)n_blocks * bs * n_kv;
   const long long bytes = type == SD_CACHE_FP4 ? tokens * (D / 2) : tokens * D * 2;

@@ -630,7 +630,7 @@ int sd_qk_rope(hipStream_t stream, int n_rows, int D, int dtype, const void* q, 
 
 /*
  * A paged cache: keys and values of one layer, [n_blocks][n_kv][block_size][D]
- * each, 16-byte aligned.  Row e of a step belongs at row_slot[e] =
+ * each; these and the scales are 16-byte aligned.  Row e of a step belongs at row_slot[e] =
  * block * block_size + offset (sd_slot_reserve's).
  *   SD_CACHE_BF16  bf16; k_scale and v_scale are not used
  *   SD_CACHE_FP4   4 bits: [n_blocks][n_kv][block_size][D / 2] bytes, the

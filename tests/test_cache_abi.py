@@ -66,7 +66,8 @@ def test_append_host_validation():
     for kw in (dict(n=-1), dict(D=60), dict(D=40, rot=40), dict(dt=2), dict(n_q=-1), dict(n_kv=0), dict(rot=12),
                dict(inter=-1), dict(eps=-1.0), dict(pos=None), dict(slot=None), dict(freq=None), dict(ctype=2),
                dict(bs=0), dict(blocks=-1), dict(q=None), dict(k=None), dict(v=None), dict(qo=None), dict(kc=None),
-               dict(vc=None), dict(ks=None), dict(vs=None), dict(kc=264), dict(vc=264), dict(v=264), dict(ld_v=120),
+               dict(vc=None), dict(ks=None), dict(vs=None), dict(kc=264), dict(vc=264),
+               dict(ks=260), dict(vs=264), dict(v=264), dict(ld_v=120),
                dict(ld_k=132), dict(ld_qo=120)):
         assert _append(**kw) == E, kw
     assert _append(D=288, ld_q=2048, ld_k=2048, ld_v=2048, ld_qo=2048) == U
@@ -86,7 +87,7 @@ def _read(n=6, D=64, ctype=C4, n_kv=2, bs=16, blocks=8, dt=BF, ld_k=128, ld_v=12
 def test_read_host_validation():
     for kw in (dict(n=-1), dict(D=60), dict(D=40), dict(dt=2), dict(n_kv=0), dict(ctype=2), dict(bs=0),
                dict(blocks=-1), dict(slot=None), dict(kc=None), dict(vc=None), dict(ks=None), dict(vs=None),
-               dict(ko=None), dict(vo=None), dict(kc=264), dict(ko=264), dict(ld_k=120), dict(ld_v=132)):
+               dict(ko=None), dict(vo=None), dict(kc=264), dict(ks=260), dict(vs=264), dict(ko=264), dict(ld_k=120), dict(ld_v=132)):
         assert _read(**kw) == E, kw
     assert _read(D=288, ld_k=2048, ld_v=2048) == U
     assert _read(n_kv=1025, ld_k=1 << 17, ld_v=1 << 17) == U
@@ -138,7 +139,7 @@ def test_attn_host_validation():
                dict(blocks=0), dict(mb=-1), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
                dict(scale=float("inf")), dict(q=None), dict(out=None), dict(kc=None), dict(vc=None), dict(ks=None),
                dict(vs=None), dict(table=None), dict(status=None), dict(ws=None), dict(q=264), dict(out=264),
-               dict(kc=264), dict(vc=264), dict(ws=128), dict(ld_q=1016), dict(ld_q=1028), dict(ld_out=1016),
+               dict(kc=264), dict(vc=264), dict(ks=260), dict(vs=264), dict(ws=128), dict(ld_q=1016), dict(ld_q=1028), dict(ld_out=1016),
                dict(ld_out=1028)):
         assert _attn(**kw) == E, kw
     for kw in (dict(D=80), dict(bs=1 << 20, mb=1 << 12), dict(bs=1 << 30, blocks=1 << 11, mb=1),
