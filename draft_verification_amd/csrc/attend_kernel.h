@@ -725,14 +725,12 @@ struct Kernel : Queries<D, NT, attn_unit(D, 64 / WT * NT, kFp4) / WT / 16, kFp4,
       // each side's buffer is given away as soon as all waves have read it, and
       // a wait leaves what is behind it on its way.  In the order of issue: keys
       // 0, values 0, keys 1, values 1, ...
-      Blocks b1 = look_up(u), b2;
+      Blocks b1 = look_up(u), b2 = look_up(u + (n > 1));
+      wait_all();   // for the queries, while the blocks are looked up
       load_side<false>(u, 0, b1);
       load_side<true>(u, 0, b1);
-      if (n > 1) {
-        b1 = look_up(u + 1);
-        load_side<false>(u + 1, 1, b1);
-      }
-      wait_all();
+      b1 = b2;
+      if (n > 1) load_side<false>(u + 1, 1, b1);
       for (int i = 0; i < n; ++i) {
         const bool more = i + 1 < n;
         if (i + 2 < n) b2 = look_up(u + i + 2);
