@@ -156,7 +156,6 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(PlanArgs a) {
 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinGrid = 2048;
-constexpr int kJoinQueries = 4;   // of a thread, whose loads are on their way together
 
 // Joins the parts of cut tiles, in the order of the runs: D / 4 threads to a
 // query and a slice of its parts (every slices-th one), slices through LDS.
@@ -166,79 +165,53 @@ constexpr int kJoinQueries = 4;   // of a thread, whose loads are on their way t
 // of 128 (64 MB at most, most of it still in the caches); latency bounds both.
 template <int D>
 __global__ __launch_bounds__(kJoinThreads) void k_join(AttnArgs a, int M) {
-  constexpr int TQ = D / 4, QB = kJoinThreads / TQ, NQ = kJoinQueries;
-  __shared__ float4 so[NQ][kJoinThreads];
-  __shared__ float2 sml[NQ][kJoinThreads];
+  constexpr int TQ = D / 4, QB = kJoinThreads / TQ;
+  __shared__ float4 so[kJoinThreads];
+  __shared__ float2 sml[kJoinThreads];
   const PlanHead& p = *a.head;
   if (!same_shape(p.shape, a.shape)) return;
   const int slices = p.slices <= QB ? p.slices : QB >= 8 ? 8 : 4;   // QB is 4 at least
-  const int per = QB / slices, jobs = (M + per * NQ - 1) / (per * NQ);
+  const int per = QB / slices, jobs = (M + per - 1) / per;
   const int mine = threadIdx.x / TQ, d = threadIdx.x % TQ * 4, slice = mine / per;
   for (long long job = blockIdx.x; job < (long long)p.n_cuts * jobs; job += gridDim.x) {
     const CutTile c = a.cuts[job / jobs];
     const Tile& t = c.tile;
     if (!in_range(a, t)) continue;   // the same for all threads
-    const int q0 = (int)(job % jobs) * per * NQ + mine % per;   // and every per-th one behind it
-    float top[NQ], l[NQ] = {};
-    float4 o[NQ];
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      top[i] = -__builtin_huge_valf();
-      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    auto add = [&](int i, float m, float sum, const float4& v) {
-      const float to = fmaxf(top[i], m), ref = to == -__builtin_huge_valf() ? 0.f : to;
-      const float f = fast_exp2(top[i] - ref), h = fast_exp2(m - ref);
-      top[i] = to;
-      l[i] = l[i] * f + sum * h;
-      o[i].x = o[i].x * f + v.x * h, o[i].y = o[i].y * f + v.y * h;
-      o[i].z = o[i].z * f + v.z * h, o[i].w = o[i].w * f + v.w * h;
+    const int q = (int)(job % jobs) * per + mine % per, qi = t.q0 + q;
+    const bool in = q < M && qi < t.queries;
+    float top = -__builtin_huge_valf(), l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float2& ml, const float4& v) {
+      const float to = fmaxf(top, ml.x), ref = to == -__builtin_huge_valf() ? 0.f : to;
+      const float f = fast_exp2(top - ref), h = fast_exp2(ml.x - ref);
+      top = to;
+      l = l * f + ml.y * h;
+      o.x = o.x * f + v.x * h, o.y = o.y * f + v.y * h;
+      o.z = o.z * f + v.z * h, o.w = o.w * f + v.w * h;
     };
     if (slice < slices) {
-#pragma unroll 2
+#pragma unroll 4
       for (int k = c.first + slice; k <= c.last; k += slices) {
-        const int64_t slot = (int64_t)(k == c.first ? 2 * k + 1 : 2 * k) * M;
-        float2 ml[NQ];
-        float4 v[NQ];
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          const int q = q0 + i * per, at = q < M && t.q0 + q < t.queries ? q : 0;   // column 0 is always a query
-          ml[i] = a.ml[slot + at];
-          v[i] = *(const float4*)(a.part + (slot + at) * D + d);
-        }
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) add(i, ml[i].x, ml[i].y, v[i]);
+        const int64_t slot = (int64_t)(k == c.first ? 2 * k + 1 : 2 * k) * M + (in ? q : 0);   // column 0 is always a query
+        add(a.ml[slot], *(const float4*)(a.part + slot * D + d));
       }
     }
     if (slices > 1) {
-#pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        so[i][threadIdx.x] = o[i];
-        sml[i][threadIdx.x] = make_float2(top[i], l[i]);
-      }
+      so[threadIdx.x] = o;
+      sml[threadIdx.x] = make_float2(top, l);
       __syncthreads();
       if (slice == 0)
-        for (int k = 1; k < slices; ++k)
-#pragma unroll
-          for (int i = 0; i < NQ; ++i) {
-            const int from = threadIdx.x + k * per * TQ;
-            add(i, sml[i][from].x, sml[i][from].y, so[i][from]);
-          }
+        for (int k = 1; k < slices; ++k) add(sml[threadIdx.x + k * per * TQ], so[threadIdx.x + k * per * TQ]);
       __syncthreads();
     }
-    if (slice > 0) continue;
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int q = q0 + i * per, qi = t.q0 + q;
-      if (q >= M || qi >= t.queries) continue;
-      const int row = qi / a.group, head = c.head * a.group + qi - row * a.group;
-      const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-      *(uint2*)(a.out + (int64_t)(t.row0 + row) * a.ld_out + (int64_t)head * D + d) =
-          make_uint2(pack_bf16(o[i].x * inv, o[i].y * inv), pack_bf16(o[i].z * inv, o[i].w * inv));
-      if (a.lse && d == 0)
-        a.lse[(int64_t)(t.row0 + row) * a.n_q + head] =
-            l[i] == 0.f ? -__builtin_huge_valf() : (top[i] + __log2f(l[i])) * 0.69314718055994531f;
-    }
+    if (slice > 0 || !in) continue;
+    const int row = qi / a.group, head = c.head * a.group + qi - row * a.group;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *(uint2*)(a.out + (int64_t)(t.row0 + row) * a.ld_out + (int64_t)head * D + d) =
+        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    if (a.lse && d == 0)
+      a.lse[(int64_t)(t.row0 + row) * a.n_q + head] =
+          l == 0.f ? -__builtin_huge_valf() : (top + __log2f(l)) * 0.69314718055994531f;
   }
 }
 
