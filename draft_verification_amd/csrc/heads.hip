@@ -102,7 +102,7 @@ enum { kToRows = 0, kToBf16 = 1, kToFp4 = 2 };
 // difference (8192 rows of 80 heads into bf16: 68 us both ways).
 // Bound by the memory and the vector units where calls are large: those rows
 // move at 4.8 TB/s, into bf16 at 4.4.  Into 4 bits the vector units alone bound
-// it (8192 rows of 16 heads: 19 us for 37 MB).  A few rows: 3.5 us, the chain
+// it (8192 rows of 16 heads: 18 us for 37 MB).  A few rows: 3.2 us, the chain
 // above.
 template <typename T, int kTo, bool kNeighbours>
 __global__ __launch_bounds__(kThreads) void k_heads(HeadArgs a) {
@@ -245,7 +245,7 @@ struct ReadArgs {
 
 // A workgroup per row, a thread per eight channels of its keys or values: the
 // row's slot is taken apart once.  8192 rows of 16 heads of 128 from 4 bits to
-// bf16: 11.6 us for 37 MB, 3.2 TB/s (13 us with a thread's row found from its
+// bf16: 12 us for 37 MB, 3.1 TB/s (13 us with a thread's row found from its
 // number), bound by loads in a chain: slot, then codes.
 template <typename T, bool kFp4>
 __global__ __launch_bounds__(kThreads) void k_cache_read(ReadArgs a) {
