@@ -321,6 +321,33 @@ def test_forms(kind, bs, D, n_q, n_kv, q_max):
                   visible(n, T, True, mask.get("window", 0)), float(np.float32(D ** -0.5)), (r, mask))
 
 
+@pytest.mark.parametrize("kind", ["fp4", "bf16"])
+def test_many_requests(kind):
+    """More requests than the plan has threads, and than there are runs."""
+    b = _batch(71, kind, 2600, 2, 2, 1, 64, 16, 1, 40)
+    got = [np64(t) for t in _attend(b)]
+    assert not got[2].any()
+    for r in range(2600):
+        n, T, r0 = int(b["n"][r]), int(b["ctx"][r]), int(b["row0"][r])
+        if n:
+            k, v = (tokens_of(x, b["table"], r, T, 16) for x in b["sides"])
+            check(got[0][r0:r0 + n], got[1][r0:r0 + n], np64(b["q"][r0:r0 + n]), k, v, visible(n, T, True, 0), 0.125, r)
+
+
+@pytest.mark.parametrize("kind", ["fp4", "bf16"])
+@pytest.mark.parametrize("n_q,n_kv,q_max", [(130, 1, 2), (1024, 2, 1), (200, 200, 1)])
+def test_many_heads(kind, n_q, n_kv, q_max):
+    """Groups of more heads than a tile has queries, and a head to each."""
+    b = _batch(61, kind, 3, q_max, n_q, n_kv, 64, 16, 1, 150)
+    got = [np64(t) for t in _attend(b)]
+    assert not got[2].any()
+    for r in range(3):
+        n, T, r0 = int(b["n"][r]), int(b["ctx"][r]), int(b["row0"][r])
+        if n:
+            k, v = (tokens_of(x, b["table"], r, T, 16) for x in b["sides"])
+            check(got[0][r0:r0 + n], got[1][r0:r0 + n], np64(b["q"])[r0:r0 + n], k, v, visible(n, T, True, 0), 0.125, r)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp4"])
 @pytest.mark.parametrize("q_max", [3, 40])
 def test_many_units_to_a_run(kind, q_max):

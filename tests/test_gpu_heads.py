@@ -253,6 +253,18 @@ def test_offsets_past_32_bits(kind):
     assert sum(int(t.count_nonzero(dim=(1, 2, 3)).count_nonzero()) for t in cache[:2]) == 6
 
 
+def test_most_heads():
+    """1024 heads of queries on one of keys, 256 channels each, two rows."""
+    g = _gen(77)
+    q, k = _heads(g, 2, 1024, 256, "bf16"), _heads(g, 2, 1, 256, "bf16")
+    w, freq, pos = torch.ones(256, device=DEV), _freq(256), torch.tensor([5, 70000], dtype=torch.int32, device=DEV)
+    r = sdv.sd_qk_rope(q, k, pos, freq, w, w)
+    torch.cuda.synchronize()
+    for x, y in ((q, r["q"]), (k, r["k"])):
+        want, size = OH.turn(_np(x), _np(w), _np(pos), _np(freq), 1e-6, False)
+        _near(_np(y), want, size, "bf16")
+
+
 def test_no_rows():
     e = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
     i = lambda dt=torch.int32: torch.empty(0, dtype=dt, device=DEV)  # noqa: E731
