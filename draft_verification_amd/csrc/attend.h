@@ -92,11 +92,13 @@ constexpr int attn_unit(int D, int M, bool fp4) {
   return fp4 ? (D <= 128 && M < 128 ? 128 : 64) : D <= 128 ? 64 : 32;
 }
 // Neighbouring tokens that are loaded with one address where they lie in one
-// block: all of a wave's quarter of a unit, or, in 4 bits, those of one load; 0: never.
+// block: all of a wave's quarter of a unit, or, in 4 bits, those of one load
+// where the quarter is longer; 0: never.
 // (bf16, an address for each piece: 518 instead of 474 us for 128 contexts of
 // one row, 263 instead of 229 for pieces of prompts.)
 constexpr int attn_span(int D, int M, bool fp4) {
-  return !fp4 ? attn_unit(D, M, fp4) / 4 : 64 % (D / 32) == 0 ? 64 / (D / 32) : 0;
+  const int quarter = attn_unit(D, M, fp4) / 4, load = 64 / (D / 32);
+  return !fp4 ? quarter : 64 % (D / 32) != 0 ? 0 : load < quarter ? load : quarter;
 }
 
 inline Cut attn_cut(int R, int q_max, int n_q, int n_kv, int D, int type, int bs) {

@@ -267,6 +267,9 @@ struct Kernel : Queries<D, NT, attn_unit(D, 64 / WT * NT, kFp4) / WT / 16, kFp4,
   static constexpr int kSpan = attn_span(D, M, kFp4);        // tokens that share one look-up of their block
   static constexpr int kSpans = kFp4 ? kPieces : 1;          // of a wave
   static_assert(TW % 16 == 0 && (kFp4 || RW * CH % 64 == 0), "unit");
+  // A wave's spans are its tokens: a longer one would begin inside another's,
+  // and end behind its block.
+  static_assert(kSpan == 0 || kSpan * kSpans == RW, "spans");
 
   // A token's chunks of 16 bytes are stored at c ^ swizzle(t), so that what one
   // access touches at a time (16 tokens of keys; 8 of values, two chunks each)
@@ -403,7 +406,7 @@ struct Kernel : Queries<D, NT, attn_unit(D, 64 / WT * NT, kFp4) / WT / 16, kFp4,
     for (int j = 0; j < kPieces; ++j) {
       if (kSpan > 0 && a.spans) {
         const uint64_t at = place(span_of(u, j), __builtin_amdgcn_readfirstlane(b.of[j]), c.bad) * DG;
-        const uint32_t mine = lane;
+        const uint32_t mine = min(lane, RW * kPer - 1);   // lanes past the wave's pieces stay in its block
         c.k[j] = ((const u32x4*)k_head + at)[mine];
         c.v[j] = ((const u32x4*)v_head + at)[mine];
         c.ks[j] = (ks_head + at)[mine];
