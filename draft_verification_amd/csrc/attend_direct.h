@@ -153,8 +153,12 @@ struct Direct : Queries<D, NT, 2, true, true, 1, 4> {
     }
   }
 
-  // bad: the chunk has a block outside the pool.
-  SDV_DEV void unit(int u, const uint8_t* chunk, bool bad) {
+  // Whether some query of the tile does not see all of a chunk's tokens.
+  SDV_DEV bool cut_by_mask(int first) const { return first + TW > all_hi || first < all_lo; }
+
+  // bad: the chunk has a block outside the pool.  Says whether values that are
+  // not finite stood beside masked weights: add_faults has to follow.
+  SDV_DEV bool unit(int u, const uint8_t* chunk, bool bad) {
     const int first = first_of(u);
     Keys k[2];
     load_keys(chunk, 0, k[0]);
@@ -174,19 +178,20 @@ struct Direct : Queries<D, NT, 2, true, true, 1, 4> {
     }
     Values c;
     load_values(chunk, c);
-    if (bad || first + TW > all_hi || first < all_lo) {
+    bool fault = false;
+    if (bad || cut_by_mask(first)) {
       this->mask(first, s);
-      uint64_t ok = ~0ull;
       if (__builtin_expect(bad, 0)) {
-        ok = this->mask_pool(first, 0, s);
+        this->mask_pool(first, 0, s);
         if (lane == 0) this->refuse();
       }
       bool odd = false;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) odd |= c.scale[i][e] == 255u;
-      if (__builtin_expect(__ballot(odd) != 0, 0)) take_out_faults(first, ok, c);
+        for (int e = 0; e < 4; ++e) odd |= c.scale[i][e] >= kFirstFault;
+      fault = __ballot(odd) != 0;
+      if (__builtin_expect(fault, 0)) take_out_faults(c);
     }
     this->move_maximum(s);
     u32x2 p[NT][NS];
@@ -211,34 +216,71 @@ struct Direct : Queries<D, NT, 2, true, true, 1, 4> {
               0, 0);
       }
     }
+    return fault;
   }
 
-  // Groups of values that are not finite (NaN, then) beside masked weights: the
-  // sums of the queries that see them become NaN, and the groups zeros (next to
-  // it: their scale becomes 2^-127).  This lane's sums are of channels
-  // ND (4 g + e) + d.
-  SDV_DEV void take_out_faults(int first, uint64_t ok, Values& c) {
-#pragma unroll 1
-    for (int i = 0; i < TW; ++i) {
-      const int tok = first + i;
-      if (tok >= ctx || !(ok >> i & 1)) continue;
-      bool bad = false;
-      const uint64_t at = place(tok, table[block_of(tok)], bad);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool fault = vs_head[at * DG + ND * (4 * g + e) / 32] == 255;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float x = fault && this->sees(tok, nt) ? __builtin_nanf("") : 0.f;
-#pragma unroll
-          for (int d = 0; d < ND; ++d) o[d][nt][e] += x;
-        }
-      }
-    }
+  // Bit 0 of each of eight codes that its scale takes past the largest bf16: by
+  // 2^126 the levels from 4 on, by 2^127 those from 2 on, all (to NaN) by 255.
+  static constexpr uint32_t kFirstFault = 253;
+  static SDV_DEV uint32_t faults(uint32_t codes, uint32_t byte) {
+    const uint32_t x = byte == 255u ? ~0u : byte == 254u ? codes >> 2 : byte == 253u ? codes >> 2 & codes >> 1 : 0u;
+    return x & 0x11111111u;
+  }
+
+  // Values that are not finite beside masked weights become zeros before the
+  // product ...
+  static SDV_DEV void take_out_faults(Values& c) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) c.scale[i][e] = c.scale[i][e] == 255u ? 0u : c.scale[i][e];
+      for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int x = 0; x < VW; ++x) c.v[i][e][x] &= ~(faults(c.v[i][e][x], c.scale[i][e]) * 15u);
+        c.scale[i][e] = c.scale[i][e] == 255u ? 0u : c.scale[i][e];
+      }
+  }
+  // ... and are added to the sums of the queries that see them, behind the last
+  // unit: they outlast any weight, and the sums' registers are the only ones
+  // that this rare path finds in use.  This lane's sums are of channels
+  // ND (4 g + e) + d.
+  SDV_DEV void add_faults(int u) {
+    const int first = first_of(u);
+    bool bad = false;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int tok = min(first + 16 * s, ctx - 1);
+      place(tok, table[block_of(tok)], bad);
+    }
+    if (!bad && !cut_by_mask(first)) return;
+#pragma unroll 1
+    for (int i = 0; i < TW; ++i) {
+      const int tok = first + i;
+      if (tok >= ctx) break;
+      bool out = false;
+      const uint64_t at = place(tok, __builtin_amdgcn_readfirstlane(table[block_of(tok)]), out);
+      if (out) continue;
+      const uint8_t* scales = vs_head + at * DG;
+      const char* codes = v_head + at * kRow;
+      int mine = 4 * g;
+      asm volatile("" : "+v"(mine));   // addresses are formed here, not kept in registers throughout
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t byte = scales[(uint32_t)(ND * (mine + e) / 32)];
+#pragma unroll
+        for (int d = 0; d < ND; d += 4) {
+          const uint32_t w = *(const uint16_t*)(codes + (uint32_t)((mine + e) * (ND / 2) + d / 2));   // four channels
+          const uint32_t fault = faults(w, byte);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t bits = byte == 255u ? 0x7FC00000u : 0x7F800000u | (w >> (4 * y + 3) & 1) << 31;
+            const float x = fault >> 4 * y & 1 ? __uint_as_float(bits) : 0.f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) o[d + y][nt][e] += this->sees(tok, nt) ? x : 0.f;
+            __builtin_amdgcn_sched_barrier(0);   // rare: few registers, not speed
+          }
+        }
+      }
+    }
   }
 
   // Until at most so many chunks, the newest, are on their way; reads of LDS
@@ -255,6 +297,7 @@ struct Direct : Queries<D, NT, 2, true, true, 1, 4> {
   // lies in its place.
   SDV_DEV void units(int u, int n) {
     uint32_t bad = 0;             // a bit for each place of the ring
+    int fault0 = n, fault1 = 0;   // the units that have faults are in [fault0, fault1)
     Base::wait_all();
     __syncthreads();              // its sums, which lay in the ring, have been read
 #pragma unroll
@@ -273,8 +316,12 @@ struct Direct : Queries<D, NT, 2, true, true, 1, 4> {
         bad = load(u + next, next % kRing) ? bad | bit : bad & ~bit;
       }
       wait_chunks(min(kRing - 1, n - 1 - i));
-      unit(u + i, sh.ring[wave][slot], (bad >> slot & 1) != 0);
+      const bool fault = unit(u + i, sh.ring[wave][slot], (bad >> slot & 1) != 0);
+      fault0 = fault ? min(fault0, i) : fault0;
+      fault1 = fault ? i + 1 : fault1;
     }
+#pragma unroll 1
+    for (int i = fault0; i < fault1; ++i) add_faults(u + i);
   }
 
   // Waves 2 and 3 into 0 and 1, then 1 into 0.

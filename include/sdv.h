@@ -642,7 +642,10 @@ int sd_qk_rope(hipStream_t stream, int n_rows, int D, int dtype, const void* q, 
  *                  2^-126) for which the group's largest magnitude is at most
  *                  7, each channel at the nearest level, ties to the even
  *                  code.  A group that is not finite gets byte 255: it reads
- *                  as NaN.
+ *                  as NaN.  What a scale takes to 2^128 or past it reads as
+ *                  infinite (the levels 4 and 6 times 2^126, those from 2 on
+ *                  times 2^127); appended magnitudes over 7 * 2^125
+ *                  (2.98e38) do.
  *
  * sd_cache_append - keys and values of a step's rows into their slots, the
  * keys normed and rotated on the way as by sd_qk_rope, the values as they are;
