@@ -181,10 +181,7 @@ struct Direct : Queries<D, NT, 2, true, true, 1, 4> {
     bool fault = false;
     if (bad || cut_by_mask(first)) {
       this->mask(first, s);
-      if (__builtin_expect(bad, 0)) {
-        this->mask_pool(first, 0, s);
-        if (lane == 0) this->refuse();
-      }
+      if (__builtin_expect(bad, 0)) this->mask_pool(first, 0, M, s);
       bool odd = false;
 #pragma unroll
       for (int i = 0; i < 2; ++i)

@@ -157,7 +157,6 @@ struct Queries {
     all_lo = window ? base + last + 1 - window : 0;
   }
 
-  SDV_DEV void refuse() const { atomicOr(a.status + req, SD_ST_BAD_INPUT); }
   SDV_DEV bool sees(int tok, int nt) const {
     return (uint32_t)tok - (uint32_t)lo[nt] < (uint32_t)hi[nt] - (uint32_t)lo[nt];
   }
@@ -176,9 +175,15 @@ struct Queries {
     }
   }
   // ... and of those outside the pool; returns which of the tokens are in it.
-  SDV_DEV uint64_t mask_pool(int first, int i0, f32x4 (&s)[NS][NT]) const {
-    const int blk = table[block_of(min(first + i0 * 16 + lane, ctx - 1))];
+  // The request is told of those that a row of the tile (M queries) sees: the
+  // others that lie in its units, behind a window, need no block.
+  SDV_DEV uint64_t mask_pool(int first, int i0, int M, f32x4 (&s)[NS][NT]) const {
+    const int tok = first + i0 * 16 + lane, blk = table[block_of(min(tok, ctx - 1))];
     const uint64_t ok = __ballot((unsigned)blk < (unsigned)a.cache.n_blocks);
+    const int base = ctx - n, to = causal ? base + (min(q0 + M, queries) - 1) / a.group + 1 : ctx;
+    const int from = window ? base + q0 / a.group + 1 - window : 0;
+    const uint64_t seen = __ballot(tok >= from && tok < to);
+    if ((~ok & seen) != 0 && lane == 0) atomicOr(a.status + req, SD_ST_BAD_INPUT);
 #pragma unroll
     for (int i = 0; i < 4 && i < NS; ++i)
 #pragma unroll
@@ -259,7 +264,7 @@ struct Kernel : Queries<D, NT, attn_unit(D, 64 / WT * NT, kFp4) / WT / 16, kFp4,
   using Base::q0, Base::queries, Base::ctx, Base::row0, Base::h, Base::req, Base::table;
   using Base::k_head, Base::v_head, Base::ks_head, Base::vs_head;
   using Base::qf, Base::o, Base::m, Base::l, Base::all_hi, Base::all_lo;
-  using Base::KS, Base::ND, Base::DG, Base::kRow, Base::block_of, Base::place, Base::refuse, Base::wait_all;
+  using Base::KS, Base::ND, Base::DG, Base::kRow, Base::block_of, Base::place, Base::wait_all;
   static constexpr int CH = D / 8;            // chunks of 16 bytes in a token's row
   static constexpr int RW = TT / 4;           // tokens of a unit that a wave loads, next to each other
   static constexpr int kPer = kFp4 ? DG : CH;                // pieces of 16 bytes in a token's row
@@ -362,10 +367,7 @@ struct Kernel : Queries<D, NT, attn_unit(D, 64 / WT * NT, kFp4) / WT / 16, kFp4,
     return b;
   }
   SDV_DEV void note_bad(bool bad, int buf) {
-    if (__builtin_expect(bad, 0)) {
-      sh.bad[buf] = 1;
-      refuse();
-    }
+    if (__builtin_expect(bad, 0)) sh.bad[buf] = 1;
   }
 
   // bf16: one side straight into LDS, a wave's 64 lanes one KB at a time.
@@ -541,8 +543,8 @@ struct Kernel : Queries<D, NT, attn_unit(D, 64 / WT * NT, kFp4) / WT / 16, kFp4,
     if (masked) {
       this->mask(u * TT + wt * TW, s);
       if (__builtin_expect(bad, 0)) {
-        ok[0] = this->mask_pool(u * TT + wt * TW, 0, s);
-        if (NS > 4) ok[1] = this->mask_pool(u * TT + wt * TW, 4, s);
+        ok[0] = this->mask_pool(u * TT + wt * TW, 0, M, s);
+        if (NS > 4) ok[1] = this->mask_pool(u * TT + wt * TW, 4, M, s);
       }
       int odd = 0;
       for (int x = tid; x < TT * CH; x += kAttnThreads) {

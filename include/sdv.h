@@ -709,14 +709,16 @@ int sd_cache_read(hipStream_t stream, int n_rows, int D, const int64_t* row_slot
  *                are in out
  *   the cache    as sd_cache_append writes it, n_blocks >= 1
  *   block_table  [R][max_blocks] int32, block_size * max_blocks below
- *                2^31 - 257.  Entries past ctx_len are not used
+ *                2^31 - 257.  Entries past ctx_len, and those of blocks of
+ *                which no row sees a token (behind a window), may hold anything
  *   scale        > 0, finite
  *   lse          [n_rows][n_q] fp32 or NULL
  *   status       [R] int32, OR-ed into (give it the plan's): BAD_INPUT where
  *                the request's rows or tokens are past the row buffers or its
- *                table's row (left as they are), or a block is outside the
- *                pool (its tokens are not seen).  Rows without slots
- *                (sd_slot_reserve's BAD_INPUT) are computed like others
+ *                table's row (left as they are), or a block of which a row
+ *                sees a token is outside the pool (its tokens are not seen
+ *                then).  Rows without slots (sd_slot_reserve's BAD_INPUT) are
+ *                computed like others
  *   workspace    the plan's, unchanged but by these calls; calls that may run
  *                at the same time need workspaces and plans of their own
  * Scores, weights' sums and outputs are held in fp32; the weights are rounded
