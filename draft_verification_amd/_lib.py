@@ -903,10 +903,11 @@ def sd_attn_plan(row0, ell, ctx_len, q_max, n_q, cache, causal=True, window=0, o
                  stream=None):
     """Cut a step's attention into equal parts, once for all its layers.  row0,
     ell, ctx_len [R] int32 as sd_slot_reserve leaves them, q_max its bound on
-    a request's rows, n_q query heads; cache: one layer's, for its sizes.
-    causal: a row sees the tokens up to its own, else all of its request's;
-    window > 0: only the last so many up to its own.  Returns a dict that
-    sd_cache_attn takes: workspace and status (device tensors) and the sizes
+    a request's rows, n_q query heads; cache: one layer's, for its type and
+    sizes (layers that differ in the type or the block size need plans of their
+    own).  causal: a row sees the tokens up to its own, else all of its
+    request's; window > 0: only the last so many up to its own.  Returns a dict
+    that sd_cache_attn takes: workspace and status (device tensors) and what
     they are for."""
     dev, device = row0.get_device(), row0.device
     R = row0.numel()
@@ -921,7 +922,8 @@ def sd_attn_plan(row0, ell, ctx_len, q_max, n_q, cache, causal=True, window=0, o
         _arg(ctx_len, i32, "ctx_len", dev, R), 1 if causal else 0, window, _arg(status, i32, "status", dev, R),
         _arg(ws, torch.uint8, "workspace", dev), ws.numel())
     _check("sd_attn_plan", code)
-    return dict(workspace=ws, status=status, R=R, q_max=q_max, n_q=n_q, n_kv=n_kv, D=D)
+    return dict(workspace=ws, status=status, R=R, q_max=q_max, n_q=n_q, n_kv=n_kv, D=D, cache_type=ctype,
+                block_size=bs)
 
 
 @_on_device
@@ -943,6 +945,10 @@ def sd_cache_attn(q, cache, block_table, plan, scale=None, lse=False, out=None, 
     if (n_q, n_kv, D, D) != (plan["n_q"], plan["n_kv"], plan["D"], c_D):
         raise ValueError(f"the plan is for {plan['n_q']} and {plan['n_kv']} heads of {plan['D']} channels, got "
                          f"{n_q} and {n_kv} of {D} and {c_D}")
+    if (ctype, bs) != (plan["cache_type"], plan["block_size"]):
+        kinds = {SD_CACHE_BF16: "bf16", SD_CACHE_FP4: "4 bits"}
+        raise ValueError(f"the plan is for a cache in {kinds[plan['cache_type']]} with blocks of {plan['block_size']}, "
+                         f"got {kinds[ctype]} and {bs}")
     R = plan["R"]
     if block_table.dim() != 2 or block_table.shape[0] != R:
         raise ValueError(f"block_table must be [R][max_blocks] with R = {R}")
