@@ -38,28 +38,31 @@ SDV_DEV T uniform(const T& v) {
 
 // 16 bytes per lane straight into LDS, from `to` of the wave on, lane after
 // lane.  Not the builtin: the compiler then waits for all loads in flight
-// before any later read of LDS, also of the other buffer.  (m0 is the compiler's to
-// set before each use, and nothing else here uses it.)  Nothing but LDS is
-// written; the callers wait (vmcnt) before the barrier that shows it to others.
+// before any later read of LDS, also of the other buffer.  Nothing but LDS and m0
+// is written; the callers wait (vmcnt) before the barrier that shows it to
+// others.
 template <bool kOnce>   // read once: streaming
 SDV_DEV void load_to_lds(const void* base, uint32_t off, uint32_t to) {   // base: the same for the wave
   if constexpr (kOnce)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(to), "v"(off), "s"(base)
-                 : "memory");
+                 : "memory", "m0");
   else
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base)
-                 : "memory");
+                 : "memory", "m0");
 }
 template <bool kOnce>
 SDV_DEV void load_to_lds(const void* from, uint32_t to) {
   if constexpr (kOnce)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(to), "v"(from) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(to), "v"(from)
+                 : "memory", "m0");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from)
+                 : "memory", "m0");
 }
 // ... and 4 bytes per lane.
 SDV_DEV void load_word_to_lds(const void* from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from)
+               : "memory", "m0");
 }
 SDV_DEV uint32_t lds_at(const void* p) { return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p; }
 
