@@ -41,13 +41,16 @@ SDV_DEV T uniform(const T& v) {
 // before any later read of LDS, also of the other buffer.  Nothing but LDS and m0
 // is written; the callers wait (vmcnt) before the barrier that shows it to
 // others.
+// Between m0 and its use there has to be one instruction, between a scalar base
+// that a vector instruction wrote (a lane's value, or one kept in a lane) and its
+// use five: the compiler sees to neither inside assembly.
 template <bool kOnce>   // read once: streaming
 SDV_DEV void load_to_lds(const void* base, uint32_t off, uint32_t to) {   // base: the same for the wave
   if constexpr (kOnce)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(to), "v"(off), "s"(base)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(to), "v"(off), "s"(base)
                  : "memory", "m0");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base)
                  : "memory", "m0");
 }
 template <bool kOnce>
