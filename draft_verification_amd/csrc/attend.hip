@@ -56,7 +56,8 @@ SDV_DEV long long block_scan(long long v, long long* part, long long* total) {
 
 // One workgroup: the tiles of all requests, the units before each of them, and
 // where every run begins.  A chain of small reads, once per step: 12 us for 4
-// requests, 17 us for 128 (some 60 layers' calls share it).
+// requests, 17 us for 128 (some 60 layers' calls share it).  One thread writes a
+// request's tiles: 62 us where a prompt of 8192 rows has 256 of them.
 __global__ __launch_bounds__(kPlanThreads) void k_plan(PlanArgs a) {
   __shared__ long long part[kPlanThreads / 64];
   const int R = a.shape.R;

@@ -15,8 +15,8 @@
 // (Values passed through LDS as bf16 cost 12 cycles of it for each KB stored and
 // 10 for each read back: 128 contexts of 1024 to 16384 tokens, one row each, 8
 // heads of 128: 177 us.  Codes straight into registers, a chunk ahead: 145 us.
-// This form: 131 us for 0.77 GB, 5.9 TB/s; the vector units, which turn codes
-// into bf16 for both products, are busy for 57 % of it.)
+// This form, alone in a trace: 133 us for 0.8 GB, 6.0 TB/s; the vector units,
+// which turn codes into bf16 for both products, are busy for 58 % of it.)
 #pragma once
 
 #include "attend_kernel.h"

@@ -242,8 +242,8 @@ struct Queries {
           w[e] = fast_exp2(fmaf(s[i][nt][e], a.scale2, -ref));
           l[nt] += w[e];
         }
-        // Rounded to bf16 for the matrix cores: 2^-9 of each weight, and the
-        // errors of different tokens do not add up.
+        // Rounded to bf16 for the matrix cores: up to 2^-8 of each weight, and
+        // the errors of different tokens do not add up.
         p[nt][i] = u32x2{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3])};
       }
     }
@@ -829,12 +829,13 @@ SDV_DEV void run_tiles(const AttnArgs& a, typename K::Shared& sh) {
   }
 }
 
-// 128 contexts of 1024 to 16384 tokens, one row each, 32 heads on 8 of 128, bf16:
-// 455 to 464 us for 2.9 GB, 6.3 TB/s, bound by the memory.  Verify rows (up to
-// 12) over 512 to 8192 tokens: 274 us for 1.45 GB, 5.3 TB/s: the beginnings of
-// tiles and the two products.  Pieces of prompts, 0.18 Tflop: 210 us, 0.84
-// Pflop/s: of a SIMD's cycles the matrix cores work for 36 %, the vector units
-// for 43 %, mostly one after the other.
+// This kernel alone, in a trace, each on one set of inputs.  128 contexts of 1024
+// to 16384 tokens, one row each, 32 heads on 8 of 128, bf16: 459 to 468 us for 2.9
+// GB, 6.3 TB/s, bound by the memory.  Verify rows (up to 12) over 512 to 8192
+// tokens: 276 to 284 us for 1.45 GB, 5.2 TB/s: the beginnings of tiles and the two
+// products.  Pieces of prompts (16 requests, up to 512 rows), 0.18 Tflop: 258 to
+// 261 us, 0.7 Pflop/s: of a SIMD's cycles the matrix cores work for 36 %, the
+// vector units for 43 %, mostly one after the other.
 template <int D, int NT, int WT, bool kFp4>
 __global__ __launch_bounds__(kAttnThreads, 2) void k_attend(AttnArgs a) {
   using K = Kernel<D, NT, WT, kFp4>;

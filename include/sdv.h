@@ -707,7 +707,8 @@ int sd_cache_read(hipStream_t stream, int n_rows, int D, const int64_t* row_slot
  *   q, out       [n_rows] rows of n_q heads, bf16, ld elements apart (ld % 8
  *                == 0), 16-byte aligned; rows of no request are left as they
  *                are in out
- *   the cache    as sd_cache_append writes it, n_blocks >= 1
+ *   the cache    as sd_cache_append writes it, n_blocks >= 1, n_kv *
+ *                block_size at most 2^31 - 257
  *   block_table  [R][max_blocks] int32, block_size * max_blocks below
  *                2^31 - 257.  Entries past ctx_len, and those of blocks of
  *                which no row sees a token (behind a window), may hold anything
