@@ -272,7 +272,7 @@ extern "C" int sd_cache_attn(hipStream_t stream, int R, int q_max, int n_q, int 
   const int rc = check_shape(R, q_max, n_q, n_kv, D, cache_type);
   if (rc != SD_OK) return rc;
   if (n_rows < 0 || block_size < 1 || n_blocks < 0 || max_blocks < 0) return SD_EINVAL;
-  if (!(scale > 0.0f && scale < __builtin_huge_valf())) return SD_EINVAL;
+  if (!(scale > 0.0f && scale * kLog2e < __builtin_huge_valf())) return SD_EINVAL;
   if ((long long)block_size * max_blocks > kMaxTokens || (long long)n_blocks * block_size > (1ll << 40) ||
       (long long)n_kv * block_size > kMaxTokens)
     return SD_EUNSUPPORTED;

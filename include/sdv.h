@@ -712,7 +712,7 @@ int sd_cache_read(hipStream_t stream, int n_rows, int D, const int64_t* row_slot
  *   block_table  [R][max_blocks] int32, block_size * max_blocks below
  *                2^31 - 257.  Entries past ctx_len, and those of blocks of
  *                which no row sees a token (behind a window), may hold anything
- *   scale        > 0, finite
+ *   scale        > 0, and scale * log2(e) finite in fp32
  *   lse          [n_rows][n_q] fp32 or NULL
  *   status       [R] int32, OR-ed into (give it the plan's): BAD_INPUT where
  *                the request's rows or tokens are past the row buffers or its
