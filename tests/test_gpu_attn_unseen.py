@@ -96,3 +96,43 @@ def test_seen_one_at_a_time(byte, D, n_q, n_kv, q_max):
         m, T, r0 = int(n[b]), int(ctx[b]), int(row0[b])
         v = tokens_of(sides[1], table, b, T, BS)[T - m:]
         assert np.array_equal(out[r0:r0 + m], np.repeat(v, n_q // n_kv, 1))
+
+
+@pytest.mark.parametrize("kind", ["fp4", "bf16"])
+@pytest.mark.parametrize("D,n_q,n_kv,q_max", FORMS)
+def test_missing_blocks(kind, D, n_q, n_kv, q_max):
+    """Blocks outside the pool while the pool's first block, nobody's, holds
+    nothing finite; one request also sees an infinite value of its own."""
+    g = gen(D + q_max + 1)
+    n, ctx, row0, table, blocks = random_batch(g, 4, q_max, q_max + 120, 300, BS, empty=False)
+    table = torch.where(table < 0, table, table + 1)
+    cache, _ = random_cache(g, kind, blocks + 1, n_kv, BS, D)
+    for side in range(2):
+        if kind == "fp4":
+            cache[2 + side][0] = torch.tensor([253, 254, 255, 253] * 4, dtype=torch.uint8, device=DEV)[None, :, None]
+        else:
+            cache[side][0] = float("inf") if side else float("nan")
+    one = int(table[2, 1])
+    if kind == "fp4":
+        cache[1][one, :, 3], cache[3][one, :, 3] = 0x7F, 253
+    else:
+        cache[1][one, :, 3] = -float("inf")
+    host = [t.cpu() for t in cache]
+    sides = [_reads(host[i].numpy(), host[2 + i].numpy()) if kind == "fp4" else np64(host[i]) for i in range(2)]
+    q = torch.randn((int(n.sum()) + 3, n_q, D), generator=g).to(torch.bfloat16).to(DEV)
+    given = table.clone()
+    given[0, 2], given[2, 4], given[3, 0] = -1, blocks + 1, 1 << 30
+    i32 = lambda t: t.to(torch.int32).to(DEV)  # noqa: E731
+    plan = sdv.sd_attn_plan(i32(row0), i32(n - 1), i32(ctx), q_max, n_q, cache)
+    r = sdv.sd_cache_attn(q, cache, given.to(DEV), plan, lse=True)
+    bad = sdv.SD_ST_BAD_INPUT
+    assert r["status"].tolist() == [bad, 0, bad, bad]
+    out, lse = np64(r["out"]), np64(r["lse"])
+    for b, gone in enumerate((2, None, 4, 0)):
+        m, T, r0 = int(n[b]), int(ctx[b]), int(row0[b])
+        k, v = (tokens_of(x, table, b, T, BS) for x in sides)
+        see = visible(m, T, True, 0)
+        if gone is not None:
+            see = see & (np.arange(T) // BS != gone)[None]
+        check(out[r0:r0 + m], lse[r0:r0 + m], np64(q)[r0:r0 + m], k, v, see, float(np.float32(D ** -0.5)), (b,))
+        assert np.isfinite(out[r0:r0 + m]).all() == (b != 2)
